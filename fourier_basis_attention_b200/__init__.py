@@ -8,6 +8,11 @@ PyTorch is used for device memory and streams. The functions keep the C names:
     fa_decode_describe, fa_decode, fa_decode_noalloc, fa_append, fa_dim_sensitivity_workspace_size,
     fa_dim_sensitivity, fa_select_dims, fa_device_status, fa_last_error
 
+and, over a paged full-precision cache,
+
+    fa_rope_init, fa_rope, fa_paged_append, fa_paged_attend_workspace_size, fa_paged_attend,
+    fa_paged_weights, fa_evict_workspace_size, fa_evict
+
 There is no CPU fallback: if the shared library is missing or fails to load, importing
 this package raises.
 """
@@ -31,7 +36,11 @@ FA_BF16, FA_F32 = 0, 1
 EXPORTED = ("fa_plan_init", "fa_plan_reserve", "fa_build_basis", "fa_compress",
             "fa_decode_workspace_size", "fa_decode", "fa_decode_noalloc", "fa_append",
             "fa_dim_sensitivity_workspace_size", "fa_dim_sensitivity", "fa_select_dims",
-            "fa_device_status", "fa_watchdog_selftest", "fa_last_error", "fa_decode_describe")
+            "fa_device_status", "fa_watchdog_selftest", "fa_last_error", "fa_decode_describe",
+            "fa_rope_init", "fa_rope", "fa_paged_append", "fa_paged_attend_workspace_size",
+            "fa_paged_attend", "fa_paged_weights", "fa_evict_workspace_size", "fa_evict")
+MAX_Q_HEADS = 1024
+ROPE_SCALINGS = {"plain": 0, "linear": 1, "ntk": 2, "bands": 3, "yarn": 4}
 NOISE_SCALE = 0.1
 NOALLOC_SCRATCH_BYTES = 16 << 20
 
@@ -79,6 +88,27 @@ class fa_cache(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in ("F_K", "F_V", "E_K", "E_V", "C_K", "C_V")]
 
 
+class fa_paged_shape(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("B", "Hq", "Hkv", "D", "page_size", "num_pages",
+                                              "max_pages", "total_q", "max_q", "max_kv")]
+
+
+class fa_paged_cache(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("K", "V", "page_table", "q_start", "kv_len")]
+
+
+class fa_rope_config(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int32) for n in ("rot_dim", "interleaved", "scaling",
+                                               "original_len")]
+                + [(n, ctypes.c_double) for n in ("base", "factor", "low", "high", "magnitude")])
+
+
+class fa_rope_plan(ctypes.Structure):
+    _fields_ = [("rot_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+                ("magnitude", ctypes.c_float), ("reserved", ctypes.c_int32),
+                ("turns", ctypes.c_uint64 * (HEAD_DIM // 2))]
+
+
 def _load() -> ctypes.CDLL:
     path = _build.LIB
     if os.environ.get("FA_SKIP_BUILD") != "1":
@@ -109,11 +139,25 @@ def configure(lib: ctypes.CDLL) -> ctypes.CDLL:
                                       I32, P]
     lib.fa_device_status.argtypes = [P]
     lib.fa_watchdog_selftest.argtypes = [ctypes.c_uint32, P]
+    SH, CA = ctypes.POINTER(fa_paged_shape), ctypes.POINTER(fa_paged_cache)
+    RP, F32 = ctypes.POINTER(fa_rope_plan), ctypes.c_float
+    lib.fa_rope_init.argtypes = [ctypes.POINTER(fa_rope_config), RP]
+    lib.fa_rope.argtypes = [RP, I32, I32, I32, P, P, ctypes.POINTER(I64), P, ctypes.POINTER(I64),
+                            I32, I32, P]
+    lib.fa_paged_append.argtypes = [SH, CA, RP, P, P, I64, P, I64, P, I64, P, I64, P]
+    lib.fa_paged_attend_workspace_size.argtypes = [SH, I32]
+    lib.fa_paged_attend_workspace_size.restype = SZ
+    lib.fa_paged_attend.argtypes = [SH, CA, P, I64, F32, I32, P, I64, P, P, SZ, P]
+    lib.fa_paged_weights.argtypes = [SH, CA, P, I64, F32, I32, P, P, I64, P]
+    lib.fa_evict_workspace_size.argtypes = [SH, I32]
+    lib.fa_evict_workspace_size.restype = SZ
+    lib.fa_evict.argtypes = [SH, CA, P, I64, I32, I32, I32, SH, CA, P, I64, P, P, P, SZ, P]
     lib.fa_last_error.argtypes = []
     lib.fa_last_error.restype = ctypes.c_char_p
     for name in ("fa_plan_init", "fa_plan_reserve", "fa_build_basis", "fa_compress", "fa_decode",
                  "fa_decode_noalloc", "fa_append", "fa_dim_sensitivity", "fa_select_dims",
-                 "fa_device_status", "fa_watchdog_selftest", "fa_decode_describe"):
+                 "fa_device_status", "fa_watchdog_selftest", "fa_decode_describe", "fa_rope_init",
+                 "fa_rope", "fa_paged_append", "fa_paged_attend", "fa_paged_weights", "fa_evict"):
         getattr(lib, name).restype = ctypes.c_int
     return lib
 
@@ -238,6 +282,212 @@ def fa_select_dims(scores, n_compressed: int) -> np.ndarray:
     mask = np.zeros((Hkv, HEAD_DIM), dtype=np.uint8)
     _check(LIB.fa_select_dims(sc.ctypes.data, Hkv, int(n_compressed), mask.ctypes.data))
     return mask
+
+
+# ------------------------------------------------------------------- paged full-precision cache
+
+def _invalid(msg: str):
+    raise FaError(FA_ERR_INVALID, msg)
+
+
+def _tensor(t, name: str, dtype, shape=None, rows: bool = False):
+    """Data pointer of a tensor on the current device. ``shape`` is compared where given
+    (None entries match anything); ``rows``: only the last two axes need to be dense."""
+    import torch
+    if not isinstance(t, torch.Tensor):
+        _invalid(f"{name} is not a tensor")
+    if t.dtype != dtype:
+        _invalid(f"{name} has dtype {t.dtype}, needs {dtype}")
+    if not t.is_cuda or t.get_device() != torch.cuda.current_device():
+        _invalid(f"{name} is on {t.device}, not on the current CUDA device")
+    if shape is not None and (t.dim() != len(shape) or any(
+            n is not None and n != m for n, m in zip(shape, t.shape))):
+        _invalid(f"{name} has shape {tuple(t.shape)}, needs {shape}")
+    if rows:
+        if t.numel() and (t.stride(-1) != 1 or (t.shape[-2] > 1 and t.stride(-2) != t.shape[-1])):
+            _invalid(f"{name}: the last two axes must be dense, strides are {t.stride()}")
+    elif not t.is_contiguous():
+        _invalid(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _token_stride(t) -> int:
+    """Elements between tokens of [tokens, heads, 128] (any value counts for a single token)."""
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * HEAD_DIM
+
+
+class PagedCache:
+    """Pools of pages: K, V bf16 [num_pages, Hkv, page_size, 128], page_table int32
+    [B, max_pages]. Keeps the tensors; a dense [B, Hkv, L, 128] tensor is a pool of B pages
+    (``PagedCache.dense``)."""
+
+    def __init__(self, K, V, page_table):
+        import torch
+        self.pointers = (_tensor(K, "K", torch.bfloat16, (None, None, None, HEAD_DIM)),
+                         _tensor(V, "V", torch.bfloat16, tuple(K.shape)),
+                         _tensor(page_table, "page_table", torch.int32, (None, None)))
+        self.K, self.V, self.page_table = K, V, page_table
+        self.num_pages, self.Hkv, self.page_size = K.shape[:3]
+        self.B, self.max_pages = page_table.shape
+
+    @classmethod
+    def dense(cls, K, V):
+        """The dense [B, Hkv, L, 128] tensors that fa_compress reads: page b is sequence b."""
+        import torch
+        table = torch.arange(K.shape[0], dtype=torch.int32, device=K.device)
+        return cls(K, V, table[:, None].contiguous())
+
+
+class PagedBatch:
+    """A batch over a PagedCache: q_start int32 [B + 1], kv_len int32 [B] (device, read when a
+    call runs) and the bounds that size the launches. max_kv = None: all the table holds."""
+
+    def __init__(self, cache: PagedCache, Hq: int, q_start, kv_len, total_q: int, max_q: int,
+                 max_kv: int | None = None):
+        import torch
+        starts = _tensor(q_start, "q_start", torch.int32, (cache.B + 1,))
+        lens = _tensor(kv_len, "kv_len", torch.int32, (cache.B,))
+        self.cache, self.q_start, self.kv_len = cache, q_start, kv_len
+        self.Hq, self.total_q = Hq, total_q
+        if max_kv is None:
+            max_kv = cache.max_pages * cache.page_size
+        self.max_kv = max_kv
+        self.shape = fa_paged_shape(cache.B, Hq, cache.Hkv, HEAD_DIM, cache.page_size,
+                                    cache.num_pages, cache.max_pages, total_q, max_q, max_kv)
+        self.c = fa_paged_cache(*cache.pointers, starts, lens)
+        self.refs = ctypes.byref(self.shape), ctypes.byref(self.c)
+
+
+def fa_rope_init(rot_dim: int = HEAD_DIM, base: float = 10000.0, interleaved: bool = False,
+                 scaling: str = "plain", factor: float = 1.0, low: float = 1.0, high: float = 4.0,
+                 original_len: int = 0, magnitude: float = 0.0) -> fa_rope_plan:
+    """Host-side plan of a rotation (see the C header for the scalings)."""
+    if scaling not in ROPE_SCALINGS:
+        _invalid(f"unknown scaling {scaling!r}")
+    config = fa_rope_config(rot_dim, int(bool(interleaved)), ROPE_SCALINGS[scaling], original_len,
+                            base, factor, low, high, magnitude)
+    plan = fa_rope_plan()
+    _check(LIB.fa_rope_init(ctypes.byref(config), ctypes.byref(plan)))
+    return plan
+
+
+_STRIDE3 = ctypes.c_int64 * 3
+
+
+def _row_ptr(t, name: str, dtype, shape):
+    """As _tensor, for tensors whose rows of 128 may lie anywhere."""
+    import torch
+    if t.dtype != dtype or t.shape != shape:
+        _invalid(f"{name} is {t.dtype} {tuple(t.shape)}, needs {dtype} {tuple(shape)}")
+    if not t.is_cuda or t.get_device() != torch.cuda.current_device():
+        _invalid(f"{name} is on {t.device}, not on the current CUDA device")
+    if t.numel() and t.stride(3) != 1:
+        _invalid(f"the last axis of {name} must be dense")
+    return t.data_ptr()
+
+
+def fa_rope(rope: fa_rope_plan, x, positions, out, transpose: bool = False, stream=None) -> None:
+    """Rotate x (bf16 or fp32 [B, T, H, 128], any strides of the first three axes) at int32
+    positions [B, T] into ``out``; ``transpose``: the transposed map, its gradient."""
+    import torch
+    if x.dtype not in (torch.bfloat16, torch.float32):
+        _invalid(f"x has dtype {x.dtype}, needs bfloat16 or float32")
+    if x.dim() != 4 or x.shape[3] != HEAD_DIM:
+        _invalid(f"x has shape {tuple(x.shape)}, needs [B, T, H, 128]")
+    B, T, H, _ = x.shape
+    px, po = _row_ptr(x, "x", x.dtype, x.shape), _row_ptr(out, "out", x.dtype, x.shape)
+    pp = _tensor(positions, "positions", torch.int32, (B, T))
+    _check(LIB.fa_rope(rope, B, T, H, pp, px, _STRIDE3(*x.stride()[:3]), po,
+                       _STRIDE3(*out.stride()[:3]), FA_F32 if x.dtype == torch.float32 else FA_BF16,
+                       int(bool(transpose)), _stream(stream)))
+
+
+def fa_paged_append(batch: PagedBatch, k, v, q=None, q_out=None, rope: fa_rope_plan | None = None,
+                    positions=None, stream=None) -> None:
+    """Write the new tokens k, v (bf16 [total_q, Hkv, 128]) into the pages; with ``rope`` k, and
+    q into q_out (bf16 [total_q, Hq, 128]), are rotated, at the cache index or ``positions``."""
+    import torch
+    bf, n, c = torch.bfloat16, batch.total_q, batch.cache
+    qs = qos = 0
+    pq = pqo = pp = None
+    if q is not None:
+        pq, qs = _tensor(q, "q", bf, (n, batch.Hq, HEAD_DIM), rows=True), _token_stride(q)
+    if q_out is not None:
+        pqo = _tensor(q_out, "q_out", bf, (n, batch.Hq, HEAD_DIM), rows=True)
+        qos = _token_stride(q_out)
+    if positions is not None:
+        pp = _tensor(positions, "positions", torch.int32, (n,))
+    pk = _tensor(k, "k", bf, (n, c.Hkv, HEAD_DIM), rows=True)
+    pv = _tensor(v, "v", bf, (n, c.Hkv, HEAD_DIM), rows=True)
+    _check(LIB.fa_paged_append(*batch.refs, rope, pp, pq, qs, pqo, qos, pk, _token_stride(k), pv,
+                               _token_stride(v), _stream(stream)))
+
+
+def fa_paged_attend_workspace_size(batch: PagedBatch, window: int = 0) -> int:
+    return LIB.fa_paged_attend_workspace_size(batch.refs[0], window)
+
+
+def _workspace(workspace):
+    import torch
+    if workspace is None:
+        return None, 0
+    if not workspace.is_cuda or workspace.get_device() != torch.cuda.current_device():
+        _invalid(f"workspace is on {workspace.device}, not on the current CUDA device")
+    if not workspace.is_contiguous():
+        _invalid("workspace must be contiguous")
+    return workspace.data_ptr() or None, workspace.numel() * workspace.element_size()
+
+
+def fa_paged_attend(batch: PagedBatch, q, out, workspace=None, lse=None, window: int = 0,
+                    scale: float = 0.0, stream=None) -> None:
+    """Causal attention of the new tokens q (bf16 [total_q, Hq, 128], rotated) over the pages,
+    their own keys included, into ``out`` (same shape); lse: fp32 [total_q, Hq] or None."""
+    import torch
+    shape = (batch.total_q, batch.Hq, HEAD_DIM)
+    pq = _tensor(q, "q", torch.bfloat16, shape, rows=True)
+    po = _tensor(out, "out", torch.bfloat16, shape, rows=True)
+    pl = None if lse is None else _tensor(lse, "lse", torch.float32, shape[:2])
+    ws, size = _workspace(workspace)
+    _check(LIB.fa_paged_attend(*batch.refs, pq, _token_stride(q), scale, window, po,
+                               _token_stride(out), pl, ws, size, _stream(stream)))
+
+
+def fa_paged_weights(batch: PagedBatch, q, lse, weights, window: int = 0, scale: float = 0.0,
+                     stream=None) -> None:
+    """Add to ``weights`` (fp32 [B, Hkv, >= max_kv]) what each key gets from the batch's
+    queries; ``lse`` as fa_paged_attend wrote it for the same arguments."""
+    import torch
+    pq = _tensor(q, "q", torch.bfloat16, (batch.total_q, batch.Hq, HEAD_DIM), rows=True)
+    pl = _tensor(lse, "lse", torch.float32, (batch.total_q, batch.Hq))
+    pw = _tensor(weights, "weights", torch.float32, (batch.cache.B, batch.cache.Hkv, None))
+    _check(LIB.fa_paged_weights(*batch.refs, pq, _token_stride(q), scale, window, pl, pw,
+                                weights.shape[2], _stream(stream)))
+
+
+def fa_evict_workspace_size(batch: PagedBatch, keep: int) -> int:
+    return LIB.fa_evict_workspace_size(batch.refs[0], keep)
+
+
+def fa_evict(batch: PagedBatch, weights, keep: int, dst: PagedCache, index, dst_len, workspace=None,
+             sink: int = 0, recent: int = 0, dst_weights=None, stream=None) -> None:
+    """Keep at most ``keep`` tokens a sequence and KV head (the first ``sink``, the last
+    ``recent``, then those of the largest ``weights``) and move them into the pages of ``dst``.
+    index: int32 [B, Hkv, keep]; dst_len: int32 [B]; dst_weights: fp32 [B, Hkv, >= keep] or None."""
+    import torch
+    c = batch.cache
+    pw = _tensor(weights, "weights", torch.float32, (c.B, c.Hkv, None))
+    pi = _tensor(index, "index", torch.int32, (c.B, c.Hkv, keep))
+    pn = _tensor(dst_len, "dst_len", torch.int32, (c.B,))
+    pd, ld = None, 0
+    if dst_weights is not None:
+        pd = _tensor(dst_weights, "dst_weights", torch.float32, (c.B, c.Hkv, None))
+        ld = dst_weights.shape[2]
+    ws, size = _workspace(workspace)
+    shape = fa_paged_shape(dst.B, dst.Hkv, dst.Hkv, HEAD_DIM, dst.page_size, dst.num_pages,
+                           dst.max_pages, 0, 0, dst.max_pages * dst.page_size)
+    cache = fa_paged_cache(*dst.pointers, None, None)
+    _check(LIB.fa_evict(*batch.refs, pw, weights.shape[2], keep, sink, recent, ctypes.byref(shape),
+                        ctypes.byref(cache), pd, ld, pi, pn, ws, size, _stream(stream)))
 
 
 def fa_device_status(stream=None) -> None:

@@ -393,6 +393,9 @@ int fa_device_status(void* stream) {
   unsigned int w = 0;
   e = fa::read_and_clear_watchdog(&w);
   if (e != cudaSuccess) return cuda_fail(e, "fa_device_status: watchdog");
+  if (w >> 8 == FA_WATCHDOG_PAGED_ENTRY)
+    return fail(FA_ERR_DEVICE, "a paged call met an entry of %s out of range",
+                (w & 0xFFu) == 1 ? "q_start or kv_len" : "page_table");
   if (w != 0)
     return fail(FA_ERR_DEVICE, "kernel %u hit the wait limit at site %u", w >> 8, w & 0xFFu);
   return FA_OK;

@@ -493,11 +493,12 @@ cudaError_t launch_watchdog_selftest(unsigned int wait_ns, cudaStream_t stream) 
 
 FA_WATCHDOG_READER(read_watchdog_compress)
 
-// The first nonzero word of the units whose kernels wait on mbarriers (compress, the
-// tensor-core decode, the cluster decode); every word is cleared.
+// The first nonzero word of the units whose kernels wait on mbarriers or check entries of a
+// paged batch; every word is cleared.
 cudaError_t read_and_clear_watchdog(unsigned int* word) {
   cudaError_t (*readers[])(unsigned int*) = {read_watchdog_compress, read_watchdog_decode_tc,
-                                             read_watchdog_decode_cl};
+                                             read_watchdog_decode_cl, read_watchdog_paged,
+                                             read_watchdog_rope, read_watchdog_evict};
   *word = 0;
   for (auto rd : readers) {
     unsigned int w = 0;
@@ -526,6 +527,8 @@ static PFN_encodeTiled get_encode_fn() {
   }
   return fn;
 }
+
+void* tensor_map_encoder() { return reinterpret_cast<void*>(get_encode_fn()); }
 
 // Token split of the compress units (one unit = one (batch, KV head) and coefficient-tile
 // pair, one CTA). When the units leave most SMs idle (small batches), each unit's token

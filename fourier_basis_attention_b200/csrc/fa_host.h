@@ -6,6 +6,9 @@
 
 #include "../../include/fourier_attention.h"
 
+// Watchdog kernel id of a paged batch's entries out of range (site 1: lengths, 2: page table).
+#define FA_WATCHDOG_PAGED_ENTRY 9u
+
 namespace fa {
 
 // Launch configuration of one fa_decode call (derived by decode_configure).
@@ -44,7 +47,37 @@ cudaError_t launch_sensitivity(const fa_plan* plan, const DecodeConfig& c, const
 cudaError_t read_and_clear_watchdog(unsigned int* word);
 cudaError_t read_watchdog_decode_tc(unsigned int* word);  // per-unit readers
 cudaError_t read_watchdog_decode_cl(unsigned int* word);
+cudaError_t read_watchdog_paged(unsigned int* word);
+cudaError_t read_watchdog_rope(unsigned int* word);
+cudaError_t read_watchdog_evict(unsigned int* word);
 cudaError_t launch_watchdog_selftest(unsigned int wait_ns, cudaStream_t stream);
+
+// Paged cache: the driver's cuTensorMapEncodeTiled (null if it has none), and the launches.
+void* tensor_map_encoder();
+int rope_init(const fa_rope_config* config, fa_rope_plan* rope);
+cudaError_t launch_rope(const fa_rope_plan* rope, int B, int T, int H, const int* positions,
+                        const void* x, const int64_t* x_stride, void* y, const int64_t* y_stride,
+                        int dtype, int transpose, cudaStream_t stream);
+cudaError_t launch_paged_append(const fa_paged_shape& s, const fa_paged_cache& c,
+                                const fa_rope_plan* rope, const int32_t* positions, const void* q,
+                                int64_t q_stride, void* q_out, int64_t q_out_stride, const void* k,
+                                int64_t k_stride, const void* v, int64_t v_stride,
+                                cudaStream_t stream);
+cudaError_t paged_attend_workspace(const fa_paged_shape& s, int window, size_t* bytes);
+cudaError_t launch_paged_attend(const fa_paged_shape& s, const fa_paged_cache& c, const void* q,
+                                int64_t q_stride, float scale, int window, void* out,
+                                int64_t out_stride, float* lse, void* workspace,
+                                cudaStream_t stream, const char** why);
+cudaError_t launch_paged_weights(const fa_paged_shape& s, const fa_paged_cache& c, const void* q,
+                                 int64_t q_stride, float scale, int window, const float* lse,
+                                 float* weights, int64_t weights_ld, cudaStream_t stream,
+                                 const char** why);
+cudaError_t evict_workspace(const fa_paged_shape& s, int keep, size_t* bytes);
+cudaError_t launch_evict(const fa_paged_shape& s, const fa_paged_cache& c, const float* weights,
+                         int64_t weights_ld, int keep, int sink, int recent,
+                         const fa_paged_shape& dst_shape, const fa_paged_cache& dst,
+                         float* dst_weights, int64_t dst_weights_ld, int32_t* index,
+                         int32_t* dst_len, void* workspace, cudaStream_t stream);
 
 // Per-device launch facts, queried once and cached (fa_runtime.cu).
 cudaError_t device_sm_count(int* sms);

@@ -1,0 +1,631 @@
+// fa_paged.cu -- attention of new tokens over a paged cache and the weights that keys gather,
+// for tiles of 16 query rows (a row = one token and one query head of a KV head).
+//
+//   o_i = sum_j exp2(c s_ij - m_i) v_j / l_i,  l_i = sum_j exp2(c s_ij - m_i),  c = scale log2 e,
+// in one pass over the keys with a running maximum m and sum l. The keys of a tile are split
+// into chunks of equal length, one CTA each; within a chunk each warp streams its own blocks
+// of 16 keys (and values) through a ring of TMA boxes and keeps its own m, l and o, so that
+// no warp waits for another until the end, when the CTA's warps merge in shared memory and
+// the chunks in a second kernel (chunk order, so repeated calls give identical bits).
+//
+// Few rows make this the read of K and V: 512 bytes a key and head against 16 x 512 flops on
+// warp-level bf16 MMA (m16n8k16; a 128-row tcgen05 tile would be 7/8 empty here).
+#include <math.h>
+#include <string.h>
+
+#include "fa_paged.cuh"
+
+namespace fa {
+
+constexpr int PR_ROWS = 16;     // query rows a tile
+constexpr int PR_KEYS = 16;     // keys a block
+constexpr int PR_WARPS = 4;
+constexpr int PR_THREADS = PR_WARPS * 32;
+constexpr int PR_BOX = PR_KEYS * 128;       // 64 dims x 16 keys
+constexpr int PR_STAGES = 3;
+constexpr int PR_STAGE = 4 * PR_BOX;        // K and V, two boxes each
+constexpr int PW_STAGES = 6;
+constexpr int PW_STAGE = 2 * PR_BOX;        // K only
+constexpr int PR_OLD = FA_HEAD_DIM + 4;     // fp32 row of the merge buffer
+constexpr int PR_RING = PR_WARPS * PR_STAGES * PR_STAGE;
+constexpr int PR_SMEM = PR_RING + 1024;
+static_assert(PR_WARPS * PW_STAGES * PW_STAGE <= PR_RING, "one shared-memory size");
+static_assert(PR_WARPS * PR_ROWS * (PR_OLD + 2) * 4 <= PR_RING, "merge buffers fit");
+
+struct RowsParams {
+  PagedBatch p;
+  int window, tiles, chunk, slots;  // tiles of rows, keys a chunk, partial results a row
+  float scale_log2;
+  const __nv_bfloat16* q;
+  long long q_stride;
+  __nv_bfloat16* out;
+  long long out_stride;
+  float* lse;
+  float* part_o;    // [row][slot][128], row = token * Hq + head
+  float2* part_ml;  // [row][slot]
+  float* weights;
+  long long weights_ld;
+};
+
+__device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                          uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+      "{%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void ldmatrix_x4_trans(uint32_t (&r)[4], const void* row) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(smem_u32(row)));
+}
+__device__ __forceinline__ float exp2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// Byte of element (row, dim) in a block of PR_KEYS rows held as two swizzled 64-dim boxes.
+__device__ __forceinline__ int box_byte(int row, int dim) {
+  return (dim >> 6) * PR_BOX + row * 128 + ((((dim & 63) >> 3) ^ (row & 7)) << 4);
+}
+
+// A fragments of 16 query rows (rows past `rows` are zero): k-step s holds dims 16 s .. + 15.
+__device__ __forceinline__ void load_q(const RowsParams& P, const SeqSpan& s, int g, int r0,
+                                       int rows, int lane, uint32_t (&qf)[8][4]) {
+  const __nv_bfloat16* src[2];
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    const int r = r0 + (lane >> 2) + 8 * u;
+    src[u] = nullptr;
+    if (r < r0 + rows)
+      src[u] = P.q + (long long)(s.q0 + r / P.p.G) * P.q_stride +
+               (g * P.p.G + r % P.p.G) * FA_HEAD_DIM + 2 * (lane & 3);
+  }
+#pragma unroll
+  for (int k = 0; k < 8; ++k)
+#pragma unroll
+    for (int v = 0; v < 4; ++v) {
+      const __nv_bfloat16* x = src[v & 1];
+      qf[k][v] = x ? *reinterpret_cast<const uint32_t*>(x + 16 * k + 8 * (v >> 1)) : 0u;
+    }
+}
+
+// scores of 16 rows x 16 keys: two accumulator fragments (keys 0-7, 8-15).
+__device__ __forceinline__ void block_scores(const uint32_t (&qf)[8][4], const uint8_t* kblk,
+                                             int lane, float (&sc)[2][4]) {
+#pragma unroll
+  for (int n = 0; n < 2; ++n)
+#pragma unroll
+    for (int v = 0; v < 4; ++v) sc[n][v] = 0.0f;
+  const int row = (lane & 7) + ((lane >> 4) << 3), dsel = ((lane >> 3) & 1) * 8;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    uint32_t b[4];
+    ldmatrix_x4(b, kblk + box_byte(row, 16 * k + dsel));
+    mma_16816(sc[0], qf[k], b[0], b[1]);
+    mma_16816(sc[1], qf[k], b[2], b[3]);
+  }
+}
+
+// A warp's ring of key blocks: blocks k0 + (w + i * PR_WARPS) * 16, i = 0, 1, ... below k_end.
+template <int STAGES, int BYTES, bool VALUES>
+struct BlockRing {
+  uint8_t* buf;
+  uint64_t* full;
+  const CUtensorMap *tk, *tv;
+  const PagedBatch* p;
+  int b, g, k0, n;  // first key of the warp, number of its blocks
+
+  __device__ void issue(int i) const {
+    const int s = i % STAGES, j = k0 + i * PR_WARPS * PR_KEYS;
+    const int pg = page_of(*p, b, j);
+    // an entry out of range reads behind the pool: the copy fills the box with zeros
+    const int row = pg < 0 ? p->num_pages * p->Hkv * p->page
+                           : (pg * p->Hkv + g) * p->page + j % p->page;
+    uint8_t* dst = buf + s * BYTES;
+    mbar_arrive_expect_tx(&full[s], BYTES);
+    tma_load_2d(dst, tk, &full[s], 0, row);
+    tma_load_2d(dst + PR_BOX, tk, &full[s], 64, row);
+    if (VALUES) {
+      tma_load_2d(dst + 2 * PR_BOX, tv, &full[s], 0, row);
+      tma_load_2d(dst + 3 * PR_BOX, tv, &full[s], 64, row);
+    }
+  }
+  // Lets copies in flight land before the CTA's shared memory goes away (abort path).
+  __device__ void drain(int from) const {
+    for (int i = from; i < min(n, from + STAGES); ++i) {
+      const unsigned long long t0 = globaltimer_ns();
+      while (!mbar_try_wait(&full[i % STAGES], (uint32_t)(i / STAGES) & 1u))
+        if (globaltimer_ns() - t0 > 200000000ull) break;
+    }
+  }
+};
+
+__global__ void __launch_bounds__(PR_THREADS, 2)
+    paged_rows_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
+                      const __grid_constant__ RowsParams P) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~uintptr_t(1023));
+  __shared__ uint64_t full[PR_WARPS][PR_STAGES];
+  __shared__ int abort_word;
+  const PagedBatch& p = P.p;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int slot = blockIdx.x % P.slots, tile = blockIdx.x / P.slots;
+  const int g = blockIdx.y, b = blockIdx.z;
+  const SeqSpan s = seq_span(p, b);
+  const int r0 = tile * PR_ROWS, rows = min(PR_ROWS, s.n * p.G - r0);
+  if (rows <= 0) return;
+  int lo, hi;
+  row_keys(s, p.G, P.window, r0, r0 + rows, &lo, &hi);
+  const bool single = P.slots == 1;
+  // chunk `slot` of the keys: chunks lie at multiples of P.chunk, the first holds lo
+  const int c0 = (lo / P.chunk + slot) * P.chunk;
+  const int k_lo = max(lo & ~(PR_KEYS - 1), c0), k_hi = min(hi, c0 + P.chunk);
+  if (k_lo >= k_hi && !(single || (slot == 0 && hi <= lo))) return;  // the merge skips it
+
+  if (threadIdx.x == 0) {
+    abort_word = 0;
+    for (int i = 0; i < PR_WARPS * PR_STAGES; ++i) mbar_init(&full[0][0] + i, 1);
+    fence_barrier_init();
+  }
+  __syncthreads();
+  volatile int* abort_flag = &abort_word;
+
+  BlockRing<PR_STAGES, PR_STAGE, true> ring;
+  ring.buf = smem + warp * PR_STAGES * PR_STAGE;
+  ring.full = full[warp];
+  ring.tk = &tk;
+  ring.tv = &tv;
+  ring.p = &p;
+  ring.b = b;
+  ring.g = g;
+  ring.k0 = k_lo + warp * PR_KEYS;
+  const int left = k_hi - ring.k0;
+  ring.n = left > 0 ? (left + PR_WARPS * PR_KEYS - 1) / (PR_WARPS * PR_KEYS) : 0;
+  if (lane == 0)
+    for (int i = 0; i < min(PR_STAGES, ring.n); ++i) ring.issue(i);
+
+  uint32_t qf[8][4];
+  load_q(P, s, g, r0, rows, lane, qf);
+  int pos[2];
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    const int r = r0 + (lane >> 2) + 8 * u;
+    pos[u] = r < r0 + rows ? s.kv - s.n + r / p.G : -1;
+  }
+  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
+  float o[16][4];
+#pragma unroll
+  for (int n = 0; n < 16; ++n)
+#pragma unroll
+    for (int v = 0; v < 4; ++v) o[n][v] = 0.0f;
+
+  for (int i = 0; i < ring.n; ++i) {
+    const int st = i % PR_STAGES;
+    const bool ok = mbar_wait(&ring.full[st], (uint32_t)(i / PR_STAGES) & 1u, abort_flag, WD_PAGED | 1u);
+    if (!__all_sync(0xFFFFFFFFu, ok)) {
+      if (lane == 0) ring.drain(i);
+      break;
+    }
+    const uint8_t* kblk = ring.buf + st * PR_STAGE;
+    const uint8_t* vblk = kblk + 2 * PR_BOX;
+    const int j0 = ring.k0 + i * PR_WARPS * PR_KEYS;
+    float sc[2][4];
+    block_scores(qf, kblk, lane, sc);
+    // edge blocks hold keys that some row does not see
+    const bool edge = j0 + PR_KEYS > s.kv - s.n + r0 / p.G + 1 ||
+                      (P.window > 0 && j0 <= s.kv - s.n + (r0 + rows - 1) / p.G - P.window);
+    float mx[2] = {m[0], m[1]};
+#pragma unroll
+    for (int n = 0; n < 2; ++n)
+#pragma unroll
+      for (int v = 0; v < 4; ++v) {
+        float x = sc[n][v] * P.scale_log2;
+        if (edge) {
+          const int j = j0 + 8 * n + 2 * (lane & 3) + (v & 1), q = pos[v >> 1];
+          if (j > q || (P.window > 0 && j <= q - P.window)) x = -INFINITY;
+        }
+        sc[n][v] = x;
+        mx[v >> 1] = fmaxf(mx[v >> 1], x);
+      }
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      mx[u] = fmaxf(mx[u], __shfl_xor_sync(0xFFFFFFFFu, mx[u], 1));
+      mx[u] = fmaxf(mx[u], __shfl_xor_sync(0xFFFFFFFFu, mx[u], 2));
+      const float base = mx[u] == -INFINITY ? 0.0f : mx[u];
+      const float f = exp2_approx(m[u] - base);
+      m[u] = mx[u];
+      l[u] *= f;
+#pragma unroll
+      for (int n = 0; n < 16; ++n) {
+        o[n][2 * u] *= f;
+        o[n][2 * u + 1] *= f;
+      }
+#pragma unroll
+      for (int n = 0; n < 2; ++n)
+#pragma unroll
+        for (int v = 2 * u; v < 2 * u + 2; ++v) {
+          sc[n][v] = exp2_approx(sc[n][v] - base);
+          l[u] += sc[n][v];
+        }
+    }
+    const uint32_t pf[4] = {pack_bf16(sc[0][0], sc[0][1]), pack_bf16(sc[0][2], sc[0][3]),
+                            pack_bf16(sc[1][0], sc[1][1]), pack_bf16(sc[1][2], sc[1][3])};
+    // values of keys outside [lo, hi) may be anything, NaN too: they count as zero
+    uint32_t keep[2] = {0xFFFFFFFFu, 0xFFFFFFFFu};
+    const bool ragged = j0 < lo || j0 + PR_KEYS > hi;
+    if (ragged) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int j = j0 + 8 * h + 2 * (lane & 3);
+        keep[h] = (j >= lo && j < hi ? 0x0000FFFFu : 0u) |
+                  (j + 1 >= lo && j + 1 < hi ? 0xFFFF0000u : 0u);
+      }
+    }
+    const int vrow = (lane & 7) + (((lane >> 3) & 1) << 3), vd = (lane >> 4) * 8;
+#pragma unroll
+    for (int n = 0; n < 16; n += 2) {
+      uint32_t v[4];
+      ldmatrix_x4_trans(v, vblk + box_byte(vrow, 8 * n + vd));
+      if (ragged) {
+        v[0] &= keep[0];
+        v[1] &= keep[1];
+        v[2] &= keep[0];
+        v[3] &= keep[1];
+      }
+      mma_16816(o[n], pf, v[0], v[1]);
+      mma_16816(o[n + 1], pf, v[2], v[3]);
+    }
+    __syncwarp();
+    if (lane == 0 && i + PR_STAGES < ring.n) ring.issue(i + PR_STAGES);
+  }
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    l[u] += __shfl_xor_sync(0xFFFFFFFFu, l[u], 1);
+    l[u] += __shfl_xor_sync(0xFFFFFFFFu, l[u], 2);
+  }
+
+  // merge the warps: o, m, l of each in shared memory (the rings are idle)
+  __syncthreads();
+  float* mo = reinterpret_cast<float*>(smem);
+  float2* ml = reinterpret_cast<float2*>(mo + PR_WARPS * PR_ROWS * PR_OLD);
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    const int r = (lane >> 2) + 8 * u;
+    float* dst = mo + (warp * PR_ROWS + r) * PR_OLD + 2 * (lane & 3);
+#pragma unroll
+    for (int n = 0; n < 16; ++n)
+      *reinterpret_cast<float2*>(dst + 8 * n) = make_float2(o[n][2 * u], o[n][2 * u + 1]);
+    if ((lane & 3) == 0) ml[warp * PR_ROWS + r] = make_float2(m[u], l[u]);
+  }
+  __syncthreads();
+  for (int w = threadIdx.x; w < rows * (FA_HEAD_DIM / 4); w += PR_THREADS) {
+    const int r = w / (FA_HEAD_DIM / 4), d = 4 * (w % (FA_HEAD_DIM / 4));
+    float mm = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < PR_WARPS; ++i) mm = fmaxf(mm, ml[i * PR_ROWS + r].x);
+    const float base = mm == -INFINITY ? 0.0f : mm;
+    float ll = 0.0f;
+    float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+    for (int i = 0; i < PR_WARPS; ++i) {
+      const float2 e = ml[i * PR_ROWS + r];
+      const float f = exp2_approx(e.x - base);
+      ll = fmaf(e.y, f, ll);
+      const float4 x = *reinterpret_cast<const float4*>(mo + (i * PR_ROWS + r) * PR_OLD + d);
+      acc.x = fmaf(x.x, f, acc.x);
+      acc.y = fmaf(x.y, f, acc.y);
+      acc.z = fmaf(x.z, f, acc.z);
+      acc.w = fmaf(x.w, f, acc.w);
+    }
+    const long long t = s.q0 + (r0 + r) / p.G;
+    const int h = g * p.G + (r0 + r) % p.G;
+    if (single) {
+      const float inv = ll > 0.0f ? 1.0f / ll : (ll == 0.0f ? 0.0f : ll);
+      *reinterpret_cast<uint2*>(P.out + t * P.out_stride + h * FA_HEAD_DIM + d) =
+          make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
+      if (d == 0 && P.lse) P.lse[t * p.Hq + h] = 0.693147180559945309f * (mm + log2f(ll));
+    } else {
+      const long long rec = (t * p.Hq + h) * P.slots + slot;
+      *reinterpret_cast<float4*>(P.part_o + rec * FA_HEAD_DIM + d) = acc;
+      if (d == 0) P.part_ml[rec] = make_float2(mm, ll);
+    }
+  }
+}
+
+// Joins the chunks of each row: one warp a row (token, head), chunks in order.
+__global__ void __launch_bounds__(256)
+    paged_join_kernel(const __grid_constant__ RowsParams P, int tile_rows) {
+  const PagedBatch& p = P.p;
+  const int lane = threadIdx.x & 31;
+  const long long row = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
+  const int t = (int)(row / p.Hq), h = (int)(row % p.Hq);
+  if (t >= p.total_q) return;
+  int b = 0;
+  for (int b0 = 0; b0 < p.B; b0 += 32) {
+    const int i = b0 + lane + 1;
+    const int n = __popc(__ballot_sync(0xFFFFFFFFu, i <= p.B && p.q_start[i] <= t));
+    b += n;
+    if (n < 32) break;
+  }
+  if (b >= p.B) return;
+  const SeqSpan s = seq_span(p, b);
+  const int i = t - s.q0;
+  if (i < 0 || i >= s.n) return;
+  const int tile = (i * p.G + h % p.G) / tile_rows;
+  int lo, hi;
+  row_keys(s, p.G, P.window, tile * tile_rows, min((tile + 1) * tile_rows, s.n * p.G), &lo, &hi);
+  const int slots = hi > lo ? (hi - 1) / P.chunk - lo / P.chunk + 1 : 1;
+  float mm = -INFINITY, ll = 0.0f;
+  float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  for (int k = 0; k < slots; ++k) {
+    const float2 e = P.part_ml[row * P.slots + k];
+    const float4 x = *reinterpret_cast<const float4*>(
+        P.part_o + (row * P.slots + k) * FA_HEAD_DIM + 4 * lane);
+    const float top = fmaxf(mm, e.x), base = top == -INFINITY ? 0.0f : top;
+    const float f = exp2_approx(mm - base), fe = exp2_approx(e.x - base);
+    mm = top;
+    ll = ll * f + e.y * fe;
+    acc.x = acc.x * f + x.x * fe;
+    acc.y = acc.y * f + x.y * fe;
+    acc.z = acc.z * f + x.z * fe;
+    acc.w = acc.w * f + x.w * fe;
+  }
+  const float inv = ll > 0.0f ? 1.0f / ll : (ll == 0.0f ? 0.0f : ll);
+  *reinterpret_cast<uint2*>(P.out + (long long)t * P.out_stride + h * FA_HEAD_DIM + 4 * lane) =
+      make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
+  if (lane == 0 && P.lse) P.lse[row] = 0.693147180559945309f * (mm + log2f(ll));
+}
+
+// Weights: a warp owns its blocks of 16 keys and runs over every tile of query rows that sees
+// them, so a key's sum is taken by one warp in one order.
+__global__ void __launch_bounds__(PR_THREADS, 2)
+    paged_weights_rows_kernel(const __grid_constant__ CUtensorMap tk,
+                              const __grid_constant__ RowsParams P) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~uintptr_t(1023));
+  __shared__ uint64_t full[PR_WARPS][PW_STAGES];
+  __shared__ int abort_word;
+  const PagedBatch& p = P.p;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int g = blockIdx.y, b = blockIdx.z;
+  const SeqSpan s = seq_span(p, b);
+  const int n_rows = s.n * p.G;
+  if (n_rows <= 0) return;
+  int lo, hi;
+  row_keys(s, p.G, P.window, 0, n_rows, &lo, &hi);
+  const int c0 = (lo / P.chunk + blockIdx.x) * P.chunk;
+  const int k_lo = max(lo & ~(PR_KEYS - 1), c0), k_hi = min(hi, c0 + P.chunk);
+  if (k_lo >= k_hi) return;
+  if (threadIdx.x == 0) {
+    abort_word = 0;
+    for (int i = 0; i < PR_WARPS * PW_STAGES; ++i) mbar_init(&full[0][0] + i, 1);
+    fence_barrier_init();
+  }
+  __syncthreads();
+  BlockRing<PW_STAGES, PW_STAGE, false> ring;
+  ring.buf = smem + warp * PW_STAGES * PW_STAGE;
+  ring.full = full[warp];
+  ring.tk = &tk;
+  ring.tv = nullptr;
+  ring.p = &p;
+  ring.b = b;
+  ring.g = g;
+  ring.k0 = k_lo + warp * PR_KEYS;
+  const int left = k_hi - ring.k0;
+  ring.n = left > 0 ? (left + PR_WARPS * PR_KEYS - 1) / (PR_WARPS * PR_KEYS) : 0;
+  if (lane == 0)
+    for (int i = 0; i < min(PW_STAGES, ring.n); ++i) ring.issue(i);
+
+  uint32_t qf[8][4];
+  float ls[2];
+  int pos[2];
+  int have = -1;
+  for (int i = 0; i < ring.n; ++i) {
+    const int st = i % PW_STAGES;
+    const bool ok = mbar_wait(&ring.full[st], (uint32_t)(i / PW_STAGES) & 1u, &abort_word, WD_PAGED | 2u);
+    if (!__all_sync(0xFFFFFFFFu, ok)) {
+      if (lane == 0) ring.drain(i);
+      break;
+    }
+    const uint8_t* kblk = ring.buf + st * PW_STAGE;
+    const int j0 = ring.k0 + i * PR_WARPS * PR_KEYS;
+    // tokens that see a key of the block: positions [j0, j0 + 15 + window)
+    const int i0 = max(0, j0 - (s.kv - s.n));
+    const int i1 = P.window > 0 ? min(s.n, j0 + PR_KEYS - 1 + P.window - (s.kv - s.n)) : s.n;
+    float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};  // keys 2 (lane & 3) + {0, 1} + {0, 8}
+    for (int tile = i0 * p.G / PR_ROWS; tile * PR_ROWS < i1 * p.G; ++tile) {
+      if (tile != have) {
+        have = tile;
+        const int r0 = tile * PR_ROWS;
+        load_q(P, s, g, r0, min(PR_ROWS, n_rows - r0), lane, qf);
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const int r = r0 + (lane >> 2) + 8 * u;
+          pos[u] = -1;
+          ls[u] = 0.0f;
+          if (r < n_rows) {
+            pos[u] = s.kv - s.n + r / p.G;
+            ls[u] = 1.44269504088896341f *
+                    P.lse[(long long)(s.q0 + r / p.G) * p.Hq + g * p.G + r % p.G];
+          }
+        }
+      }
+      float sc[2][4];
+      block_scores(qf, kblk, lane, sc);
+#pragma unroll
+      for (int n = 0; n < 2; ++n)
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+          const int j = j0 + 8 * n + 2 * (lane & 3) + (v & 1), q = pos[v >> 1];
+          const bool seen = j <= q && !(P.window > 0 && j <= q - P.window);
+          if (seen) sum[2 * n + (v & 1)] += exp2_approx(fmaf(sc[n][v], P.scale_log2, -ls[v >> 1]));
+        }
+    }
+#pragma unroll
+    for (int v = 0; v < 4; ++v)
+#pragma unroll
+      for (int x = 4; x < 32; x <<= 1) sum[v] += __shfl_xor_sync(0xFFFFFFFFu, sum[v], x);
+    if (lane < 4) {
+      float* w = P.weights + ((long long)b * p.Hkv + g) * P.weights_ld;
+#pragma unroll
+      for (int v = 0; v < 4; ++v) {
+        const int j = j0 + 2 * lane + (v & 1) + 8 * (v >> 1);
+        if (j >= lo && j < hi) w[j] += sum[v];
+      }
+    }
+    __syncwarp();
+    if (lane == 0 && i + PW_STAGES < ring.n) ring.issue(i + PW_STAGES);
+  }
+}
+
+FA_WATCHDOG_READER(read_watchdog_paged)
+
+// ------------------------------------------------------------------------- host side
+PagedBatch paged_batch(const fa_paged_shape& s, const fa_paged_cache& c) {
+  PagedBatch p;
+  p.table = c.page_table;
+  p.q_start = c.q_start;
+  p.kv_len = c.kv_len;
+  p.B = s.B;
+  p.Hq = s.Hq;
+  p.Hkv = s.Hkv;
+  p.G = s.Hq / s.Hkv;
+  p.page = s.page_size;
+  p.num_pages = s.num_pages;
+  p.max_pages = s.max_pages;
+  p.total_q = s.total_q;
+  p.max_q = s.max_q;
+  p.max_kv = s.max_kv;
+  return p;
+}
+
+bool encode_pool(CUtensorMap* map, const void* pool, const fa_paged_shape& s, int rows) {
+  const auto encode = reinterpret_cast<decltype(&cuTensorMapEncodeTiled)>(tensor_map_encoder());
+  if (!encode) return false;
+  cuuint64_t dims[2] = {FA_HEAD_DIM, (cuuint64_t)s.num_pages * s.Hkv * s.page_size};
+  cuuint64_t strides[1] = {FA_HEAD_DIM * 2};
+  cuuint32_t box[2] = {64, (cuuint32_t)rows};
+  cuuint32_t estr[2] = {1, 1};
+  return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(pool), dims, strides,
+                box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Keys a chunk: two CTAs to an SM (what shared memory holds) for the widest batch the shape
+// allows, in multiples of 64 keys, at least 256 (below that the merge costs more than the
+// chunk's own read).
+static int rows_chunk(const fa_paged_shape& s, int tiles, int sms) {
+  const long long units = (long long)s.B * s.Hkv * tiles;
+  const long long want = (2LL * sms + units - 1) / units;
+  long long c = (s.max_kv + want - 1) / want;
+  c = (c + 63) / 64 * 64;
+  return (int)(c < 256 ? 256 : c);
+}
+
+// Chunks that the keys of one tile can touch: the cache, or the tile's tokens and the window.
+static int rows_slots(const fa_paged_shape& s, int window, int chunk, int tile_rows) {
+  const int G = s.Hq / s.Hkv;
+  long long n = (s.max_kv + chunk - 1) / chunk;
+  if (window > 0) {
+    const long long span = (long long)window + (tile_rows + G - 1) / G;
+    const long long m = (span + chunk - 1) / chunk + 1;
+    n = m < n ? m : n;
+  }
+  return (int)(n < 1 ? 1 : n);
+}
+
+static cudaError_t rows_plan(const fa_paged_shape& s, int window, RowsParams* P, size_t* bytes) {
+  int sms = 148;
+  cudaError_t e = device_sm_count(&sms);
+  if (e != cudaSuccess) return e;
+  const int G = s.Hq / s.Hkv;
+  P->tiles = (int)(((long long)(s.max_q < s.total_q ? s.max_q : s.total_q) * G + PR_ROWS - 1) / PR_ROWS);
+  P->chunk = rows_chunk(s, P->tiles, sms);
+  P->slots = rows_slots(s, window, P->chunk, PR_ROWS);
+  P->window = window;
+  *bytes = P->slots == 1 ? 0
+                         : (size_t)s.total_q * s.Hq * P->slots * (FA_HEAD_DIM * sizeof(float) + sizeof(float2));
+  return cudaSuccess;
+}
+
+cudaError_t paged_attend_workspace(const fa_paged_shape& s, int window, size_t* bytes) {
+  RowsParams P;
+  return rows_plan(s, window, &P, bytes);
+}
+
+cudaError_t launch_paged_attend(const fa_paged_shape& s, const fa_paged_cache& c, const void* q,
+                                int64_t q_stride, float scale, int window, void* out,
+                                int64_t out_stride, float* lse, void* workspace,
+                                cudaStream_t stream, const char** why) {
+  RowsParams P;
+  memset(&P, 0, sizeof(P));
+  size_t bytes = 0;
+  cudaError_t e = rows_plan(s, window, &P, &bytes);
+  if (e != cudaSuccess) return e;
+  P.p = paged_batch(s, c);
+  P.scale_log2 = scale * 1.44269504088896341f;
+  P.q = static_cast<const __nv_bfloat16*>(q);
+  P.q_stride = q_stride;
+  P.out = static_cast<__nv_bfloat16*>(out);
+  P.out_stride = out_stride;
+  P.lse = lse;
+  const size_t recs = (size_t)s.total_q * s.Hq * P.slots;
+  P.part_o = static_cast<float*>(workspace);
+  P.part_ml = reinterpret_cast<float2*>(P.part_o + recs * FA_HEAD_DIM);
+  CUtensorMap tk, tv;
+  if (!encode_pool(&tk, c.K, s, PR_KEYS) || !encode_pool(&tv, c.V, s, PR_KEYS)) {
+    *why = "cuTensorMapEncodeTiled rejected the pools";
+    return cudaErrorInvalidValue;
+  }
+  if ((e = raise_smem_limit(reinterpret_cast<const void*>(paged_rows_kernel), PR_SMEM)) != cudaSuccess)
+    return e;
+  const dim3 grid((unsigned)(P.slots * P.tiles), (unsigned)s.Hkv, (unsigned)s.B);
+  paged_rows_kernel<<<grid, PR_THREADS, PR_SMEM, stream>>>(tk, tv, P);
+  if ((e = cudaGetLastError()) != cudaSuccess || P.slots == 1) return e;
+  const long long rows = (long long)s.total_q * s.Hq;
+  paged_join_kernel<<<(unsigned)((rows + 7) / 8), 256, 0, stream>>>(P, PR_ROWS);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_paged_weights(const fa_paged_shape& s, const fa_paged_cache& c, const void* q,
+                                 int64_t q_stride, float scale, int window, const float* lse,
+                                 float* weights, int64_t weights_ld, cudaStream_t stream,
+                                 const char** why) {
+  RowsParams P;
+  memset(&P, 0, sizeof(P));
+  int sms = 148;
+  cudaError_t e = device_sm_count(&sms);
+  if (e != cudaSuccess) return e;
+  P.p = paged_batch(s, c);
+  P.window = window;
+  P.scale_log2 = scale * 1.44269504088896341f;
+  P.q = static_cast<const __nv_bfloat16*>(q);
+  P.q_stride = q_stride;
+  P.lse = const_cast<float*>(lse);
+  P.weights = weights;
+  P.weights_ld = weights_ld;
+  P.chunk = rows_chunk(s, 1, sms);
+  P.slots = rows_slots(s, window, P.chunk, (s.max_q < s.total_q ? s.max_q : s.total_q) * P.p.G);
+  CUtensorMap tk;
+  if (!encode_pool(&tk, c.K, s, PR_KEYS)) {
+    *why = "cuTensorMapEncodeTiled rejected the pool";
+    return cudaErrorInvalidValue;
+  }
+  const void* fn = reinterpret_cast<const void*>(paged_weights_rows_kernel);
+  if ((e = raise_smem_limit(fn, PR_SMEM)) != cudaSuccess) return e;
+  const dim3 grid((unsigned)P.slots, (unsigned)s.Hkv, (unsigned)s.B);
+  paged_weights_rows_kernel<<<grid, PR_THREADS, PR_SMEM, stream>>>(tk, P);
+  return cudaGetLastError();
+}
+
+}  // namespace fa

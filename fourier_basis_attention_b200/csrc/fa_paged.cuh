@@ -1,0 +1,71 @@
+// fa_paged.cuh -- what the kernels over a paged cache share: the batch on the device, the
+// key range of a tile of query rows, and the tensor map of a pool.
+#pragma once
+
+#include <cuda.h>
+
+#include "fa_host.h"
+#include "fa_internal.cuh"
+
+namespace fa {
+
+// Watchdog sites of the paged calls (kernel ids of fa_device_status).
+enum : unsigned int {
+  WD_PAGED = 8u << 8,        // waits of the paged attention kernels
+  WD_PAGED_ENTRY = FA_WATCHDOG_PAGED_ENTRY << 8,  // a device-side entry out of range
+  WD_ENTRY_LENGTH = WD_PAGED_ENTRY | 1u,  // q_start / kv_len
+  WD_ENTRY_PAGE = WD_PAGED_ENTRY | 2u,    // page_table
+};
+
+struct PagedBatch {
+  const int* table;
+  const int* q_start;
+  const int* kv_len;
+  int B, Hq, Hkv, G, page, num_pages, max_pages, total_q, max_q, max_kv;
+};
+
+// New tokens [q0, q0 + n) of a sequence and its cached tokens kv (the new ones included).
+struct SeqSpan {
+  int q0, n, kv;
+};
+
+__device__ __forceinline__ void flag_entry(unsigned int site) { atomicCAS(&g_watchdog, 0u, site); }
+
+// The span of sequence b; one whose entries break the shape's bounds is empty and flagged.
+__device__ __forceinline__ SeqSpan seq_span(const PagedBatch& p, int b) {
+  SeqSpan s;
+  s.q0 = p.q_start[b];
+  const int end = p.q_start[b + 1];
+  s.kv = p.kv_len[b];
+  s.n = end - s.q0;
+  if (s.q0 < 0 || end < s.q0 || end > p.total_q || s.n > p.max_q || s.kv < 0 || s.kv > p.max_kv) {
+    flag_entry(WD_ENTRY_LENGTH);
+    s.q0 = s.n = s.kv = 0;
+  }
+  return s;
+}
+
+// The page that holds cached token j of sequence b; -1 (flagged) if the entry is out of range.
+__device__ __forceinline__ int page_of(const PagedBatch& p, int b, int j) {
+  const int pg = p.table[(long long)b * p.max_pages + j / p.page];
+  if ((unsigned)pg < (unsigned)p.num_pages) return pg;
+  flag_entry(WD_ENTRY_PAGE);
+  return -1;
+}
+
+// Keys [lo, hi) that the query rows [r0, r1) of a sequence see, rows numbered token * G +
+// head (r1 <= n * G). Empty: hi <= lo.
+__device__ __forceinline__ void row_keys(const SeqSpan& s, int G, int window, int r0, int r1,
+                                         int* lo, int* hi) {
+  const int first = s.kv - s.n + r0 / G, last = s.kv - s.n + (r1 - 1) / G;
+  *hi = last + 1;
+  *lo = window > 0 ? max(0, first - window + 1) : 0;
+}
+
+// 2-D map of a pool: rows of 128 bf16 in (page, head, slot) order, boxes of 64 dims x `rows`
+// rows in the 128-byte swizzle.
+bool encode_pool(CUtensorMap* map, const void* pool, const fa_paged_shape& s, int rows);
+
+PagedBatch paged_batch(const fa_paged_shape& s, const fa_paged_cache& c);
+
+}  // namespace fa

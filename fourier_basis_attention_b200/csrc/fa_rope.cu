@@ -1,0 +1,337 @@
+// fa_rope.cu -- rotary positions, alone and fused with the write of new tokens into pages.
+//
+// Pair (a, b) at position p: (a, b) -> m (a cos t - b sin t, b cos t + a sin t), t = p f.
+// The phase is exact: f / (2 pi) is held as a 64-bit fraction of a turn, so the low 64 bits
+// of p * turns are the turn's fraction for every int32 position, and sincospif takes its top
+// 32 bits (an fp32 product p * f is off by 0.03 radians at a million positions).
+//
+// Memory-bound: each row is read and written once. A CTA takes RT tokens: its threads first
+// put the tokens' 64 (cos, sin) pairs into shared memory (one sincospif a pair and token, shared by
+// all heads), then walk over (token, head, item), an item being the two 16-byte vectors
+// that hold 8 (bf16) or 4 (fp32) pairs. A rot_dim whose halves are not whole vectors takes
+// items of one pair instead.
+#include <math.h>
+#include <string.h>
+
+#include "fa_paged.cuh"
+
+namespace fa {
+
+constexpr int RP_THREADS = 256;
+constexpr int RP_PAIRS = FA_HEAD_DIM / 2;
+
+struct RopeParams {
+  int rot, interleaved, transpose;
+  float magnitude;
+  unsigned long long turns[RP_PAIRS];
+};
+
+// magnitude * (cos, sin) of pair i at position pos.
+__device__ __forceinline__ float2 rope_cs(const RopeParams& r, int i, int pos) {
+  const unsigned long long phase = (unsigned long long)(long long)pos * r.turns[i];
+  // nearest quarter turn, and the rest in [-1/4, 1/4] half turns: fp32 holds that to 2^-26
+  const uint32_t turn = (uint32_t)(phase >> 32), quarter = (turn + 0x20000000u) >> 30;
+  float s, c;
+  sincospif((float)(int)(turn - (quarter << 30)) * 4.656612873077393e-10f, &s, &c);  // * 2^-31
+  if (quarter & 1u) {
+    const float t = c;
+    c = -s;
+    s = t;
+  }
+  if (quarter & 2u) {
+    c = -c;
+    s = -s;
+  }
+  return make_float2(r.magnitude * c, r.magnitude * (r.transpose ? -s : s));
+}
+
+template <typename T>
+struct RopeVec;
+template <>
+struct RopeVec<float> {
+  static constexpr int N = 4;
+  __device__ static void load(const float* p, float* v) {
+    const float4 x = *reinterpret_cast<const float4*>(p);
+    v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
+  }
+  __device__ static void store(float* p, const float* v) {
+    *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+  }
+  __device__ static float get(float x) { return x; }
+  __device__ static float put(float x) { return x; }
+};
+template <>
+struct RopeVec<__nv_bfloat16> {
+  static constexpr int N = 8;
+  __device__ static void load(const __nv_bfloat16* p, float* v) {
+    const uint4 x = *reinterpret_cast<const uint4*>(p);
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = __uint_as_float(w[i] << 16);
+      v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    }
+  }
+  __device__ static void store(__nv_bfloat16* p, const float* v) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+      w[i] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+    *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  __device__ static float get(__nv_bfloat16 x) { return __bfloat162float(x); }
+  __device__ static __nv_bfloat16 put(float x) { return __float2bfloat16_rn(x); }
+};
+
+// Item `it` of a row: rotated pairs first, then the dims that pass. VECTOR: N pairs (two
+// vectors) or two vectors of passing dims; else one pair / two dims. cs: the token's pairs.
+template <typename T, bool VECTOR>
+__device__ __forceinline__ void rope_item(const T* x, T* y, int it, int rot, int interleaved,
+                                          const float2* cs) {
+  using V = RopeVec<T>;
+  constexpr int N = VECTOR ? V::N : 1;
+  const int i = it * N;  // first pair, or half the first passing dim
+  const bool turn = 2 * i < rot;
+  int da = 2 * i, db = 2 * i + N;
+  if (turn && !interleaved) {
+    da = i;
+    db = rot / 2 + i;
+  }
+  if constexpr (VECTOR) {
+    float a[N], b[N];
+    V::load(x + da, a);
+    V::load(x + db, b);
+    if (turn) {
+      if (interleaved) {
+#pragma unroll
+        for (int e = 0; e < N; e += 2) {
+          const float2 u = cs[i + e / 2], w = cs[i + (N + e) / 2];
+          const float a0 = a[e], b0 = b[e];
+          a[e] = a0 * u.x - a[e + 1] * u.y;
+          a[e + 1] = a[e + 1] * u.x + a0 * u.y;
+          b[e] = b0 * w.x - b[e + 1] * w.y;
+          b[e + 1] = b[e + 1] * w.x + b0 * w.y;
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < N; ++e) {
+          const float2 u = cs[i + e];
+          const float a0 = a[e];
+          a[e] = a0 * u.x - b[e] * u.y;
+          b[e] = b[e] * u.x + a0 * u.y;
+        }
+      }
+    }
+    V::store(y + da, a);
+    V::store(y + db, b);
+  } else {
+    const T xa = x[da], xb = x[db];
+    if (turn) {
+      const float2 u = cs[i];
+      const float a = V::get(xa), b = V::get(xb);
+      y[da] = V::put(a * u.x - b * u.y);
+      y[db] = V::put(b * u.x + a * u.y);
+    } else {
+      y[da] = xa;
+      y[db] = xb;
+    }
+  }
+}
+
+template <typename T, bool VECTOR, int RT>
+__global__ void __launch_bounds__(RP_THREADS)
+    rope_kernel(const __grid_constant__ RopeParams r, const T* x, T* y,
+                const int* __restrict__ positions, long long n_tokens, int T_len, int H,
+                long long xb, long long xt, long long xh, long long yb, long long yt,
+                long long yh) {
+  __shared__ float2 cs[RT][RP_PAIRS];
+  const long long n0 = (long long)blockIdx.x * RT;
+  const int nt = (int)min((long long)RT, n_tokens - n0);
+  for (int i = threadIdx.x; i < nt * (r.rot / 2); i += RP_THREADS) {
+    const int t = i / (r.rot / 2), pair = i - t * (r.rot / 2);
+    cs[t][pair] = rope_cs(r, pair, positions[n0 + t]);
+  }
+  __syncthreads();
+  constexpr int ITEMS = RP_PAIRS / (VECTOR ? RopeVec<T>::N : 1);
+  for (int w = threadIdx.x; w < nt * H * ITEMS; w += RP_THREADS) {
+    const int it = w % ITEMS, row = w / ITEMS, h = row / nt, t = row - h * nt;
+    const long long n = n0 + t, b = n / T_len, tt = n - b * T_len;
+    rope_item<T, VECTOR>(x + b * xb + tt * xt + h * xh, y + b * yb + tt * yt + h * yh, it, r.rot,
+                         r.interleaved, cs[t]);
+  }
+}
+
+struct AppendRows {
+  const __nv_bfloat16 *q, *k, *v;
+  __nv_bfloat16 *q_out, *K, *V;
+  long long q_stride, q_out_stride, k_stride, v_stride;
+  const int* positions;
+  int heads;  // q heads to rotate (0 without q) + Hkv keys + Hkv values
+  int rotate;
+};
+
+// One CTA a token: its sequence (the count of starts <= t; all threads look at once), its
+// slot, its angles, then its rows.
+template <bool VECTOR>
+__global__ void __launch_bounds__(RP_THREADS)
+    paged_append_kernel(const __grid_constant__ RopeParams r, const __grid_constant__ PagedBatch p,
+                        const __grid_constant__ AppendRows a) {
+  __shared__ float2 cs[RP_PAIRS];
+  const int t = blockIdx.x;
+  int b = 0;
+  for (int b0 = 0; b0 < p.B; b0 += RP_THREADS) {
+    const int i = b0 + threadIdx.x + 1;
+    const int n = __syncthreads_count(i <= p.B && p.q_start[i] <= t);
+    b += n;
+    if (n < RP_THREADS) break;
+  }
+  if (b >= p.B) return;  // a row behind the last sequence
+  const SeqSpan s = seq_span(p, b);
+  const int i = t - s.q0;
+  if (i < 0 || i >= s.n) return;
+  const int j = s.kv - s.n + i;  // cache index
+  if (a.rotate) {
+    if (threadIdx.x < r.rot / 2)
+      cs[threadIdx.x] = rope_cs(r, threadIdx.x, a.positions ? a.positions[t] : j);
+    __syncthreads();
+  }
+  long long slot = -1;  // row of the pools, head 0
+  if (j >= 0) {
+    const int pg = page_of(p, b, j);
+    if (pg >= 0) slot = (long long)pg * p.Hkv * p.page + j % p.page;
+  }
+  constexpr int ITEMS = RP_PAIRS / (VECTOR ? RopeVec<__nv_bfloat16>::N : 1);
+  const int nq = a.heads - 2 * p.Hkv;
+  const int rot = a.rotate ? r.rot : 0;
+  for (int w = threadIdx.x; w < a.heads * ITEMS; w += RP_THREADS) {
+    const int it = w % ITEMS, h = w / ITEMS;
+    const __nv_bfloat16* x;
+    __nv_bfloat16* y;
+    if (h < nq) {
+      x = a.q + (long long)t * a.q_stride + h * FA_HEAD_DIM;
+      y = a.q_out + (long long)t * a.q_out_stride + h * FA_HEAD_DIM;
+    } else {
+      if (slot < 0) break;  // not cached: the rest of the items are keys and values too
+      const int g = h - nq, gk = g < p.Hkv ? g : g - p.Hkv;
+      x = g < p.Hkv ? a.k + (long long)t * a.k_stride + gk * FA_HEAD_DIM
+                    : a.v + (long long)t * a.v_stride + gk * FA_HEAD_DIM;
+      y = (g < p.Hkv ? a.K : a.V) + (slot + (long long)gk * p.page) * FA_HEAD_DIM;
+    }
+    rope_item<__nv_bfloat16, VECTOR>(x, y, it, h < nq + p.Hkv ? rot : 0, r.interleaved, cs);
+  }
+}
+
+FA_WATCHDOG_READER(read_watchdog_rope)
+
+// ------------------------------------------------------------------------- host side
+int rope_init(const fa_rope_config* c, fa_rope_plan* rope) {
+  const double pi = 3.14159265358979323846;
+  const int n = c->rot_dim / 2;
+  double base = c->base;
+  if (c->scaling == FA_ROPE_NTK && c->rot_dim > 2)
+    base *= pow(c->factor, (double)c->rot_dim / (c->rot_dim - 2));
+  double a = 0.0, z = 0.0;  // FA_ROPE_YARN: the pairs between which the blend falls
+  if (c->scaling == FA_ROPE_YARN) {
+    const double per = c->rot_dim / (2.0 * log(base));
+    a = fmax(0.0, floor(per * log(c->original_len / (c->high * 2.0 * pi))));
+    z = fmin(c->rot_dim - 1.0, ceil(per * log(c->original_len / (c->low * 2.0 * pi))));
+    z = fmax(z, a + 0.001);
+  }
+  memset(rope, 0, sizeof(*rope));
+  rope->rot_dim = c->rot_dim;
+  rope->interleaved = c->interleaved;
+  const double own = c->scaling == FA_ROPE_YARN ? 0.1 * log(c->factor) + 1.0 : 1.0;
+  rope->magnitude = (float)(c->magnitude > 0.0 ? c->magnitude : own);
+  for (int i = 0; i < n; ++i) {
+    double f = pow(base, -2.0 * i / c->rot_dim);
+    if (c->scaling == FA_ROPE_LINEAR) f /= c->factor;
+    if (c->scaling == FA_ROPE_BANDS || c->scaling == FA_ROPE_YARN) {
+      double w = c->scaling == FA_ROPE_BANDS
+                     ? (c->original_len * f / (2.0 * pi) - c->low) / (c->high - c->low)
+                     : 1.0 - (i - a) / (z - a);
+      w = fmin(1.0, fmax(0.0, w));
+      f = f / c->factor * (1.0 - w) + f * w;
+    }
+    const long double turn = (long double)f / 6.283185307179586476925286766559L;
+    rope->turns[i] = (uint64_t)(turn * 18446744073709551616.0L);
+  }
+  return FA_OK;
+}
+
+static RopeParams rope_params(const fa_rope_plan* rope, int transpose) {
+  RopeParams r;
+  memset(&r, 0, sizeof(r));
+  if (!rope) return r;
+  r.rot = rope->rot_dim;
+  r.interleaved = rope->interleaved;
+  r.transpose = transpose;
+  r.magnitude = rope->magnitude;
+  for (int i = 0; i < RP_PAIRS; ++i) r.turns[i] = rope->turns[i];
+  return r;
+}
+
+// Pairs in whole vectors of n elements: the halves (or the interleaved run) hold a multiple
+// of n pairs.
+static bool rope_vectors(const RopeParams& r, int n) { return (r.rot / 2) % n == 0; }
+
+template <typename T>
+static cudaError_t rope_typed(const RopeParams& r, int B, int T_len, int H, const int* positions,
+                              const void* x, const int64_t* xs, void* y, const int64_t* ys,
+                              cudaStream_t stream) {
+  const long long n = (long long)B * T_len;
+  int sms = 148;
+  cudaError_t e = device_sm_count(&sms);
+  if (e != cudaSuccess) return e;
+  const bool vec = rope_vectors(r, RopeVec<T>::N);
+  // 4 tokens a CTA share the set-up once they still fill every SM several times
+  const bool four = n >= 16LL * sms;
+  auto go = [&](auto kernel, int rt) {
+    kernel<<<(unsigned)((n + rt - 1) / rt), RP_THREADS, 0, stream>>>(
+        r, static_cast<const T*>(x), static_cast<T*>(y), positions, n, T_len, H, xs[0], xs[1], xs[2],
+        ys[0], ys[1], ys[2]);
+    return cudaGetLastError();
+  };
+  if (vec) return four ? go(rope_kernel<T, true, 4>, 4) : go(rope_kernel<T, true, 1>, 1);
+  return four ? go(rope_kernel<T, false, 4>, 4) : go(rope_kernel<T, false, 1>, 1);
+}
+
+cudaError_t launch_rope(const fa_rope_plan* rope, int B, int T_len, int H, const int* positions,
+                        const void* x, const int64_t* xs, void* y, const int64_t* ys, int dtype,
+                        int transpose, cudaStream_t stream) {
+  const RopeParams r = rope_params(rope, transpose);
+  return dtype == FA_F32
+             ? rope_typed<float>(r, B, T_len, H, positions, x, xs, y, ys, stream)
+             : rope_typed<__nv_bfloat16>(r, B, T_len, H, positions, x, xs, y, ys, stream);
+}
+
+cudaError_t launch_paged_append(const fa_paged_shape& s, const fa_paged_cache& c,
+                                const fa_rope_plan* rope, const int32_t* positions, const void* q,
+                                int64_t q_stride, void* q_out, int64_t q_out_stride, const void* k,
+                                int64_t k_stride, const void* v, int64_t v_stride,
+                                cudaStream_t stream) {
+  const RopeParams r = rope_params(rope, 0);
+  AppendRows a;
+  a.q = static_cast<const __nv_bfloat16*>(q);
+  a.k = static_cast<const __nv_bfloat16*>(k);
+  a.v = static_cast<const __nv_bfloat16*>(v);
+  a.q_out = static_cast<__nv_bfloat16*>(q_out);
+  a.K = static_cast<__nv_bfloat16*>(c.K);
+  a.V = static_cast<__nv_bfloat16*>(c.V);
+  a.q_stride = q_stride;
+  a.q_out_stride = q_out_stride;
+  a.k_stride = k_stride;
+  a.v_stride = v_stride;
+  a.positions = positions;
+  a.heads = (q ? s.Hq : 0) + 2 * s.Hkv;
+  a.rotate = rope ? 1 : 0;
+  const PagedBatch p = paged_batch(s, c);
+  if (rope_vectors(r, RopeVec<__nv_bfloat16>::N))
+    paged_append_kernel<true><<<(unsigned)s.total_q, RP_THREADS, 0, stream>>>(r, p, a);
+  else
+    paged_append_kernel<false><<<(unsigned)s.total_q, RP_THREADS, 0, stream>>>(r, p, a);
+  return cudaGetLastError();
+}
+
+}  // namespace fa

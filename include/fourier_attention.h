@@ -48,7 +48,8 @@ enum fa_status {
   FA_ERR_INVALID = 1,     /* bad argument: null/misaligned pointer, inconsistent shape */
   FA_ERR_UNSUPPORTED = 2, /* valid but outside what the kernels implement (D != 128, ...) */
   FA_ERR_CUDA = 3,        /* a CUDA runtime/driver call or launch failed */
-  FA_ERR_DEVICE = 4       /* a kernel's bounded wait expired (see fa_device_status) */
+  FA_ERR_DEVICE = 4       /* a kernel's bounded wait expired, or a paged call met a page or
+                             length out of range (see fa_device_status) */
 };
 
 enum fa_dtype { FA_BF16 = 0, FA_F32 = 1 };
@@ -342,12 +343,206 @@ int fa_dim_sensitivity(const fa_shape* shape, const void* q, const void* K, cons
  */
 int fa_select_dims(const float* scores, int32_t Hkv, int32_t n_compressed, uint8_t* mask_out);
 
+/* ---------------------------------------------------------------------------------------
+ * Paged cache: the full-precision cache while a prompt is read, and of sequences that are
+ * too short or too young to compress.
+ * (The paper starts from a finished K, V cache. These entry points make one: positions are
+ * rotated into queries and keys, keys and values are written into pages, the new tokens
+ * attend over the pages, and the attention weight that each key has gathered decides which
+ * tokens stay. A dense [B][Hkv][L][128] tensor, what fa_compress reads, is a pool of B
+ * pages of L tokens, so fa_evict moves a paged cache into it.)
+ *
+ * Pools. K and V are bf16 [num_pages][Hkv][page_size][128]. Token j of sequence b is slot
+ *   j % page_size of page page_table[b][j / page_size].
+ * Batch. q_start [B + 1] and kv_len [B] are device int32. The rows of sequence b in q, k, v
+ *   and out are [q_start[b], q_start[b + 1]): its n new tokens. kv_len[b] counts its cached
+ *   tokens with the new ones, so new token i sits at cache index p = kv_len[b] - n + i. An
+ *   index p < 0 (a sequence with fewer cached than new tokens, such as a padded one with
+ *   kv_len 0) names a token that is not cached: it is not written and it sees no key.
+ *   q_start[0] = 0, q_start ascends, and rows at and behind q_start[B] are left as they
+ *   were. A sequence may have no new token.
+ * Both arrays, the table and the positions are read on the device, so that a captured CUDA
+ * graph replays with new lengths; max_q and max_kv bound them and size the launches.
+ * Entries that break a bound (a page outside the pool that a token needs, n > max_q,
+ * kv_len > max_kv, q_start outside [0, total_q] or descending) never lead to an access out
+ * of range: that sequence's results are unspecified and the next fa_device_status returns
+ * FA_ERR_DEVICE.
+ * ------------------------------------------------------------------------------------- */
+
+/* Shape of a paged batch (host). B sequences (at most 65535); Hq query heads over Hkv KV
+ * heads (Hq % Hkv == 0, Hq at most FA_MAX_Q_HEADS), D = 128; num_pages pages of page_size
+ * tokens; max_pages entries in a row of page_table; total_q rows of q, k, v and out; no
+ * sequence has more than max_q new or max_kv cached tokens. max_kv <= max_pages * page_size,
+ * below 2^30; num_pages * Hkv * page_size < 2^31; total_q * Hq < 2^30. */
+#define FA_MAX_Q_HEADS 1024
+typedef struct fa_paged_shape {
+  int32_t B, Hq, Hkv, D, page_size, num_pages, max_pages, total_q, max_q, max_kv;
+} fa_paged_shape;
+
+/* Device buffers of a paged batch: the pools, page_table [B][max_pages], q_start [B + 1],
+ * kv_len [B] (the int32 arrays 4-byte aligned). */
+typedef struct fa_paged_cache {
+  void* K;
+  void* V;
+  const int32_t* page_table;
+  const int32_t* q_start;
+  const int32_t* kv_len;
+} fa_paged_cache;
+
+/*
+ * Rotary positions. Pair i of the first rot_dim dims of a row at position p turns by the
+ * angle p f_i; the other dims pass. Pairs are (i, i + rot_dim / 2), or (2 i, 2 i + 1) when
+ * interleaved. With (a, b) the pair, m the magnitude:
+ *   a' = m (a cos(p f_i) - b sin(p f_i)),   b' = m (b cos(p f_i) + a sin(p f_i)).
+ * Frequencies f_i = base^(-2 i / rot_dim), i < rot_dim / 2, scaled for contexts `factor`
+ * times longer than `original_len`:
+ *   FA_ROPE_PLAIN   as they are;
+ *   FA_ROPE_LINEAR  f_i / factor;
+ *   FA_ROPE_NTK     base replaced by base * factor^(rot_dim / (rot_dim - 2));
+ *   FA_ROPE_BANDS   with r = original_len f_i / (2 pi) turns over the original length and
+ *                   w = clamp((r - low) / (high - low), 0, 1): f_i (w + (1 - w) / factor);
+ *   FA_ROPE_YARN    the same blend with w falling linearly in i from 1 at the pair that turns
+ *                   `high` times (its index rounded down) to 0 at the one that turns `low`
+ *                   times (rounded up).
+ * magnitude = 0 picks 1, or 0.1 ln(factor) + 1 for FA_ROPE_YARN.
+ */
+enum fa_rope_scaling {
+  FA_ROPE_PLAIN = 0,
+  FA_ROPE_LINEAR = 1,
+  FA_ROPE_NTK = 2,
+  FA_ROPE_BANDS = 3,
+  FA_ROPE_YARN = 4
+};
+typedef struct fa_rope_config {
+  int32_t rot_dim;      /* even, 2 .. 128 */
+  int32_t interleaved;  /* 0 or 1 */
+  int32_t scaling;      /* enum fa_rope_scaling */
+  int32_t original_len; /* FA_ROPE_BANDS, FA_ROPE_YARN: >= 1 */
+  double base;          /* > 1 */
+  double factor;        /* >= 1 */
+  double low, high;     /* FA_ROPE_BANDS, FA_ROPE_YARN: 0 < low < high */
+  double magnitude;     /* >= 0; 0 = the scaling's own */
+} fa_rope_config;
+
+/* turns[i] = f_i / (2 pi) in units of 2^-64: the phase of position p is the low 64 bits of
+ * p * turns[i], exact in integers for every int32 position (negative ones too). */
+typedef struct fa_rope_plan {
+  int32_t rot_dim, interleaved;
+  float magnitude;
+  int32_t reserved;
+  uint64_t turns[FA_HEAD_DIM / 2];
+} fa_rope_plan;
+
+/* fa_rope_init -- the plan of a configuration. Pure host function. FA_ERR_INVALID for
+ * values outside the ranges above. */
+int fa_rope_init(const fa_rope_config* config, fa_rope_plan* rope);
+
+/*
+ * fa_rope -- rotate rows of 128 dims.
+ *   x, y       device [B][T][H][128] of dtype (FA_BF16 or FA_F32), dims contiguous; the
+ *              element strides of the first three axes are x_stride[3] and y_stride[3]
+ *              (host), each a multiple of 16 bytes and >= 0. Rows of y must not overlap
+ *              (an order of the axes exists in which each stride covers the ones inside);
+ *              x may repeat rows (stride 0). y may be x with the same strides; any other
+ *              overlap of the two is undefined.
+ *   positions  device int32 [B][T], any values.
+ *   transpose  0, or 1 for the transposed map (angle negated, same magnitude): the gradient
+ *              of the rotation; with magnitude 1 it takes the positions out again.
+ * B, T, H >= 0; a call with no rows does nothing. Products and sums in fp32.
+ */
+int fa_rope(const fa_rope_plan* rope, int32_t B, int32_t T, int32_t H, const int32_t* positions,
+            const void* x, const int64_t* x_stride, void* y, const int64_t* y_stride,
+            int32_t dtype, int32_t transpose, void* stream);
+
+/*
+ * fa_paged_append -- write the new tokens of a batch into the pages, rotated on the way.
+ *   rope       plan applied to q and k, or NULL: k is written as it is.
+ *   positions  device int32 [total_q], or NULL: the cache index of each token. (A cache that
+ *              fa_evict has cut has fewer tokens than positions: pass them then.)
+ *   q, q_out   device bf16 [total_q][Hq][128] with token strides q_stride, q_out_stride (in
+ *              elements), or both NULL. q_out = rotated q; q_out may be q (same stride).
+ *              Without rope they must be NULL.
+ *   k, v       device bf16 [total_q][Hkv][128] with token strides k_stride, v_stride.
+ * Token strides are multiples of 8, at least heads * 128. Two sequences (or two slots of
+ * one) must not share a page that is written. Launches one kernel.
+ */
+int fa_paged_append(const fa_paged_shape* shape, const fa_paged_cache* cache,
+                    const fa_rope_plan* rope, const int32_t* positions, const void* q,
+                    int64_t q_stride, void* q_out, int64_t q_out_stride, const void* k,
+                    int64_t k_stride, const void* v, int64_t v_stride, void* stream);
+
+/*
+ * fa_paged_attend -- causal attention of the new tokens over the pages (their own keys and
+ * values, already written, included): a prompt chunk, single decode tokens, or both in one
+ * batch.
+ *   q        device bf16 [total_q][Hq][128], token stride q_stride (a multiple of 8,
+ *            >= Hq * 128).
+ *   scale    softmax scale, finite and >= 0; 0 picks 1/sqrt(128).
+ *   window   0: the token at cache index p sees keys j <= p; > 0: p - window < j <= p.
+ *   out      device bf16 [total_q][Hq][128], token stride out_stride.
+ *   lse      device fp32 [total_q][Hq] or NULL: log of the sum of exp(score), the scores
+ *            scaled; natural logarithm. Rows that see no key get out = 0, lse = -infinity.
+ * fp32 scores, maxima and sums; the weights are rounded to bf16 before the product with V
+ * (the tensor cores take both operands in one type) and out once at the end. What lies in
+ * pages behind kv_len, or before the window of a sequence's first new token, is never used,
+ * NaN or not; the keys and values between must be finite. page_size must be a multiple of 16,
+ * or at least max_kv (one page a sequence); FA_ERR_UNSUPPORTED otherwise.
+ *   workspace  device scratch of at least fa_paged_attend_workspace_size(shape, window)
+ *            bytes (may be 0: then workspace may be NULL). Calls that may overlap, captured
+ *            graphs included, need one each.
+ */
+size_t fa_paged_attend_workspace_size(const fa_paged_shape* shape, int32_t window);
+int fa_paged_attend(const fa_paged_shape* shape, const fa_paged_cache* cache, const void* q,
+                    int64_t q_stride, float scale, int32_t window, void* out, int64_t out_stride,
+                    float* lse, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * fa_paged_weights -- add the attention weight that each key gets from the batch's queries:
+ *   weights[b][g][j] += sum over new tokens i that see j and heads h of KV head g of
+ *                       exp(scale q_ih . k_j - lse_ih).
+ *   lse      device fp32 [total_q][Hq], as fa_paged_attend wrote it for the same call.
+ *   weights  device fp32 [B][Hkv][weights_ld], weights_ld >= max_kv; entries j >= kv_len[b]
+ *            are left as they were.
+ * Other arguments as for fa_paged_attend (V and out are not touched). One CTA owns a key:
+ * no atomics, repeated calls give identical bits.
+ */
+int fa_paged_weights(const fa_paged_shape* shape, const fa_paged_cache* cache, const void* q,
+                     int64_t q_stride, float scale, int32_t window, const float* lse,
+                     float* weights, int64_t weights_ld, void* stream);
+
+/*
+ * fa_evict -- keep at most `keep` tokens of every sequence, per KV head: its first `sink`
+ * tokens, its last `recent` ones, and of the others those with the largest weights (equal
+ * weights: the lower index first; NaN ranks behind every number). Kept tokens move to the
+ * front of the pages of `dst`, in order. A sequence of at most `keep` tokens is copied whole.
+ *   shape, cache  the source batch; q_start, total_q and max_q are not used (cache->q_start
+ *            may be NULL).
+ *   weights  device fp32 [B][Hkv][weights_ld], weights_ld >= max_kv.
+ *   keep     >= 1, sink, recent >= 0, sink + recent <= keep.
+ *   dst_shape, dst_cache  pools, table and page sizes of the destination (any page_size;
+ *            B, Hkv, D as in shape; max_kv >= keep; K, V and page_table are used). Its pages
+ *            must not be pages that the call reads; two sequences must not share one.
+ *   dst_weights  device fp32 [B][Hkv][dst_weights_ld] or NULL: weights of the kept tokens.
+ *   index    device int32 [B][Hkv][keep]: cache index of each kept token, ascending, -1 behind
+ *            the last.
+ *   dst_len  device int32 [B]: min(kv_len, keep); may be dst_cache->kv_len.
+ * Destination slots and weights behind the kept tokens are left as they were.
+ *   workspace  at least fa_evict_workspace_size(shape, keep) bytes (may be 0, then may be
+ *            NULL); calls that may overlap need one each.
+ */
+size_t fa_evict_workspace_size(const fa_paged_shape* shape, int32_t keep);
+int fa_evict(const fa_paged_shape* shape, const fa_paged_cache* cache, const float* weights,
+             int64_t weights_ld, int32_t keep, int32_t sink, int32_t recent,
+             const fa_paged_shape* dst_shape, const fa_paged_cache* dst_cache, float* dst_weights,
+             int64_t dst_weights_ld, int32_t* index, int32_t* dst_len, void* workspace,
+             size_t workspace_bytes, void* stream);
+
 /*
  * fa_device_status -- synchronise `stream`, then read and clear the library's kernel
  * watchdog word. Returns FA_OK if no kernel launched since the last call hit a wait
- * limit, FA_ERR_DEVICE (message names the kernel and wait) if one did, FA_ERR_CUDA if
- * the stream reported an error. Kernels that hit a limit stop their work, release their
- * tensor memory and return instead of hanging.
+ * limit or met a page or length out of range, FA_ERR_DEVICE (message names the kernel and
+ * the wait or entry) if one did, FA_ERR_CUDA if the stream reported an error. Kernels that
+ * hit a limit stop their work, release their tensor memory and return instead of hanging.
  */
 int fa_device_status(void* stream);
 
