@@ -10,7 +10,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libfourier_attention.so")
 SOURCES = ["fa_abi.cu", "fa_basis.cu", "fa_compress.cu", "fa_decode.cu", "fa_decode_tc.cu", "fa_decode_hmma.cu", "fa_decode_cl.cu", "fa_runtime.cu", "fa_append.cu", "fa_sensitivity.cu",
-           "fa_noalloc.cu", "fa_rope.cu", "fa_paged.cu", "fa_evict.cu", "fa_paged_abi.cu"]
+           "fa_noalloc.cu", "fa_rope.cu", "fa_paged.cu", "fa_paged_tc.cu", "fa_evict.cu", "fa_paged_abi.cu"]
 HEADERS = ["fa_paged.cuh", "fa_internal.cuh", "fa_host.h", "fa_decode_common.cuh"]
 PUBLIC_HEADER = os.path.join(ROOT, "include", "fourier_attention.h")
 

@@ -498,6 +498,7 @@ FA_WATCHDOG_READER(read_watchdog_compress)
 cudaError_t read_and_clear_watchdog(unsigned int* word) {
   cudaError_t (*readers[])(unsigned int*) = {read_watchdog_compress, read_watchdog_decode_tc,
                                              read_watchdog_decode_cl, read_watchdog_paged,
+                                             read_watchdog_paged_tc,
                                              read_watchdog_rope, read_watchdog_evict};
   *word = 0;
   for (auto rd : readers) {

@@ -48,6 +48,7 @@ cudaError_t read_and_clear_watchdog(unsigned int* word);
 cudaError_t read_watchdog_decode_tc(unsigned int* word);  // per-unit readers
 cudaError_t read_watchdog_decode_cl(unsigned int* word);
 cudaError_t read_watchdog_paged(unsigned int* word);
+cudaError_t read_watchdog_paged_tc(unsigned int* word);
 cudaError_t read_watchdog_rope(unsigned int* word);
 cudaError_t read_watchdog_evict(unsigned int* word);
 cudaError_t launch_watchdog_selftest(unsigned int wait_ns, cudaStream_t stream);

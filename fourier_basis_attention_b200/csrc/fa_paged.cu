@@ -35,17 +35,25 @@ static_assert(PR_WARPS * PR_ROWS * (PR_OLD + 2) * 4 <= PR_RING, "merge buffers f
 struct RowsParams {
   PagedBatch p;
   int window, tiles, chunk, slots;  // tiles of rows, keys a chunk, partial results a row
+  int max_rows;  // sequences of more rows a KV head are another kernel's (0: none are)
   float scale_log2;
   const __nv_bfloat16* q;
   long long q_stride;
   __nv_bfloat16* out;
   long long out_stride;
   float* lse;
-  float* part_o;    // [row][slot][128], row = token * Hq + head
+  float* part_o;    // [row][slot][128], row as part_row gives it
   float2* part_ml;  // [row][slot]
   float* weights;
   long long weights_ld;
 };
+
+// Partial results are numbered by (token, head), or, where only sequences of at most max_rows
+// rows have some, by (sequence, KV head, row): max_q bounds a batch of long sequences too.
+__device__ __forceinline__ long long part_row(const PagedBatch& p, int max_rows, int b, int g,
+                                              long long token, int head, int row) {
+  return max_rows > 0 ? ((long long)b * p.Hkv + g) * max_rows + row : token * p.Hq + head;
+}
 
 __device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
                                           uint32_t b1) {
@@ -60,16 +68,6 @@ __device__ __forceinline__ void ldmatrix_x4_trans(uint32_t (&r)[4], const void* 
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
                : "r"(smem_u32(row)));
 }
-__device__ __forceinline__ float exp2_approx(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
-
 // Byte of element (row, dim) in a block of PR_KEYS rows held as two swizzled 64-dim boxes.
 __device__ __forceinline__ int box_byte(int row, int dim) {
   return (dim >> 6) * PR_BOX + row * 128 + ((((dim & 63) >> 3) ^ (row & 7)) << 4);
@@ -161,7 +159,7 @@ __global__ void __launch_bounds__(PR_THREADS, 2)
   const int g = blockIdx.y, b = blockIdx.z;
   const SeqSpan s = seq_span(p, b);
   const int r0 = tile * PR_ROWS, rows = min(PR_ROWS, s.n * p.G - r0);
-  if (rows <= 0) return;
+  if (rows <= 0 || (P.max_rows > 0 && s.n * p.G > P.max_rows)) return;
   int lo, hi;
   row_keys(s, p.G, P.window, r0, r0 + rows, &lo, &hi);
   const bool single = P.slots == 1;
@@ -333,35 +331,57 @@ __global__ void __launch_bounds__(PR_THREADS, 2)
           make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
       if (d == 0 && P.lse) P.lse[t * p.Hq + h] = 0.693147180559945309f * (mm + log2f(ll));
     } else {
-      const long long rec = (t * p.Hq + h) * P.slots + slot;
+      const long long rec = part_row(p, P.max_rows, b, g, t, h, r0 + r) * P.slots + slot;
       *reinterpret_cast<float4*>(P.part_o + rec * FA_HEAD_DIM + d) = acc;
       if (d == 0) P.part_ml[rec] = make_float2(mm, ll);
     }
   }
 }
 
-// Joins the chunks of each row: one warp a row (token, head), chunks in order.
-__global__ void __launch_bounds__(256)
-    paged_join_kernel(const __grid_constant__ RowsParams P, int tile_rows) {
+struct JoinParams {
+  PagedBatch p;
+  int window, chunk, slots;
+  int tile_rows;           // rows whose keys were split together
+  int max_rows, min_rows;  // as RowsParams::max_rows; rows of a sequence must exceed min_rows
+  const float* part_o;
+  const float2* part_ml;
+  __nv_bfloat16* out;
+  long long out_stride;
+  float* lse;
+};
+
+// Joins the chunks of each row: one warp a row, chunks in order.
+__global__ void __launch_bounds__(256) paged_join_kernel(const __grid_constant__ JoinParams P) {
   const PagedBatch& p = P.p;
   const int lane = threadIdx.x & 31;
   const long long row = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
-  const int t = (int)(row / p.Hq), h = (int)(row % p.Hq);
-  if (t >= p.total_q) return;
-  int b = 0;
-  for (int b0 = 0; b0 < p.B; b0 += 32) {
-    const int i = b0 + lane + 1;
-    const int n = __popc(__ballot_sync(0xFFFFFFFFu, i <= p.B && p.q_start[i] <= t));
-    b += n;
-    if (n < 32) break;
+  int b = 0, r, g;  // sequence, row of it in its KV head
+  SeqSpan s;
+  if (P.max_rows > 0) {
+    r = (int)(row % P.max_rows);
+    g = (int)(row / P.max_rows % p.Hkv);
+    b = (int)(row / P.max_rows / p.Hkv);
+    if (b >= p.B) return;
+    s = seq_span(p, b);
+    if (r >= s.n * p.G || s.n * p.G > P.max_rows) return;
+  } else {
+    const int t = (int)(row / p.Hq), h = (int)(row % p.Hq);
+    if (t >= p.total_q) return;
+    for (int b0 = 0; b0 < p.B; b0 += 32) {
+      const int i = b0 + lane + 1;
+      const int n = __popc(__ballot_sync(0xFFFFFFFFu, i <= p.B && p.q_start[i] <= t));
+      b += n;
+      if (n < 32) break;
+    }
+    if (b >= p.B) return;
+    s = seq_span(p, b);
+    if (t < s.q0 || t - s.q0 >= s.n || s.n * p.G <= P.min_rows) return;
+    g = h / p.G;
+    r = (t - s.q0) * p.G + h % p.G;
   }
-  if (b >= p.B) return;
-  const SeqSpan s = seq_span(p, b);
-  const int i = t - s.q0;
-  if (i < 0 || i >= s.n) return;
-  const int tile = (i * p.G + h % p.G) / tile_rows;
+  const int tile = r / P.tile_rows;
   int lo, hi;
-  row_keys(s, p.G, P.window, tile * tile_rows, min((tile + 1) * tile_rows, s.n * p.G), &lo, &hi);
+  row_keys(s, p.G, P.window, tile * P.tile_rows, min((tile + 1) * P.tile_rows, s.n * p.G), &lo, &hi);
   const int slots = hi > lo ? (hi - 1) / P.chunk - lo / P.chunk + 1 : 1;
   float mm = -INFINITY, ll = 0.0f;
   float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
@@ -378,10 +398,12 @@ __global__ void __launch_bounds__(256)
     acc.z = acc.z * f + x.z * fe;
     acc.w = acc.w * f + x.w * fe;
   }
+  const long long t = s.q0 + r / p.G;
+  const int h = g * p.G + r % p.G;
   const float inv = ll > 0.0f ? 1.0f / ll : (ll == 0.0f ? 0.0f : ll);
-  *reinterpret_cast<uint2*>(P.out + (long long)t * P.out_stride + h * FA_HEAD_DIM + 4 * lane) =
+  *reinterpret_cast<uint2*>(P.out + t * P.out_stride + h * FA_HEAD_DIM + 4 * lane) =
       make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
-  if (lane == 0 && P.lse) P.lse[row] = 0.693147180559945309f * (mm + log2f(ll));
+  if (lane == 0 && P.lse) P.lse[t * p.Hq + h] = 0.693147180559945309f * (mm + log2f(ll));
 }
 
 // Weights: a warp owns its blocks of 16 keys and runs over every tile of query rows that sees
@@ -532,46 +554,61 @@ static int rows_chunk(const fa_paged_shape& s, int tiles, int sms) {
   return (int)(c < 256 ? 256 : c);
 }
 
-// Chunks that the keys of one tile can touch: the cache, or the tile's tokens and the window.
-static int rows_slots(const fa_paged_shape& s, int window, int chunk, int tile_rows) {
-  const int G = s.Hq / s.Hkv;
-  long long n = (s.max_kv + chunk - 1) / chunk;
+int chunk_slots(const fa_paged_shape& s, int window, int chunk, int tokens) {
+  long long n = ((long long)s.max_kv + chunk - 1) / chunk;
   if (window > 0) {
-    const long long span = (long long)window + (tile_rows + G - 1) / G;
+    const long long span = (long long)window + tokens;
     const long long m = (span + chunk - 1) / chunk + 1;
     n = m < n ? m : n;
   }
   return (int)(n < 1 ? 1 : n);
 }
 
-static cudaError_t rows_plan(const fa_paged_shape& s, int window, RowsParams* P, size_t* bytes) {
+// How a call runs: tensor-core tiles for sequences of more than 16 rows a KV head, 16-row tiles
+// for the others (for all of them where the heads of one token do not fit a tile).
+struct AttendPlan {
+  TilePlan t;
+  RowsParams r;
+  size_t rows_records;
+};
+
+static cudaError_t attend_plan(const fa_paged_shape& s, int window, AttendPlan* a, size_t* bytes) {
   int sms = 148;
   cudaError_t e = device_sm_count(&sms);
   if (e != cudaSuccess) return e;
+  if ((e = tile_plan(s, window, &a->t)) != cudaSuccess) return e;
   const int G = s.Hq / s.Hkv;
-  P->tiles = (int)(((long long)(s.max_q < s.total_q ? s.max_q : s.total_q) * G + PR_ROWS - 1) / PR_ROWS);
+  const long long rows = (long long)(s.max_q < s.total_q ? s.max_q : s.total_q) * G;
+  RowsParams* P = &a->r;
+  memset(P, 0, sizeof(*P));
+  P->max_rows = a->t.tok > 0 || rows <= PR_ROWS ? PR_ROWS : 0;
+  P->tiles = P->max_rows > 0 ? 1 : (int)((rows + PR_ROWS - 1) / PR_ROWS);
   P->chunk = rows_chunk(s, P->tiles, sms);
-  P->slots = rows_slots(s, window, P->chunk, PR_ROWS);
+  P->slots = chunk_slots(s, window, P->chunk, (PR_ROWS + G - 1) / G);
   P->window = window;
-  *bytes = P->slots == 1 ? 0
-                         : (size_t)s.total_q * s.Hq * P->slots * (FA_HEAD_DIM * sizeof(float) + sizeof(float2));
+  a->rows_records = 0;
+  if (P->slots > 1)
+    a->rows_records = (P->max_rows > 0 ? (size_t)s.B * s.Hkv * PR_ROWS : (size_t)s.total_q * s.Hq) * P->slots;
+  *bytes = (a->rows_records + a->t.records) * (FA_HEAD_DIM * sizeof(float) + sizeof(float2));
   return cudaSuccess;
 }
 
 cudaError_t paged_attend_workspace(const fa_paged_shape& s, int window, size_t* bytes) {
-  RowsParams P;
-  return rows_plan(s, window, &P, bytes);
+  AttendPlan a;
+  return attend_plan(s, window, &a, bytes);
 }
 
 cudaError_t launch_paged_attend(const fa_paged_shape& s, const fa_paged_cache& c, const void* q,
                                 int64_t q_stride, float scale, int window, void* out,
                                 int64_t out_stride, float* lse, void* workspace,
                                 cudaStream_t stream, const char** why) {
-  RowsParams P;
-  memset(&P, 0, sizeof(P));
+  AttendPlan a;
   size_t bytes = 0;
-  cudaError_t e = rows_plan(s, window, &P, &bytes);
+  cudaError_t e = attend_plan(s, window, &a, &bytes);
   if (e != cudaSuccess) return e;
+  float* part_o = static_cast<float*>(workspace);
+  float2* part_ml = reinterpret_cast<float2*>(part_o + (a.rows_records + a.t.records) * FA_HEAD_DIM);
+  RowsParams& P = a.r;
   P.p = paged_batch(s, c);
   P.scale_log2 = scale * 1.44269504088896341f;
   P.q = static_cast<const __nv_bfloat16*>(q);
@@ -579,9 +616,8 @@ cudaError_t launch_paged_attend(const fa_paged_shape& s, const fa_paged_cache& c
   P.out = static_cast<__nv_bfloat16*>(out);
   P.out_stride = out_stride;
   P.lse = lse;
-  const size_t recs = (size_t)s.total_q * s.Hq * P.slots;
-  P.part_o = static_cast<float*>(workspace);
-  P.part_ml = reinterpret_cast<float2*>(P.part_o + recs * FA_HEAD_DIM);
+  P.part_o = part_o;
+  P.part_ml = part_ml;
   CUtensorMap tk, tv;
   if (!encode_pool(&tk, c.K, s, PR_KEYS) || !encode_pool(&tv, c.V, s, PR_KEYS)) {
     *why = "cuTensorMapEncodeTiled rejected the pools";
@@ -591,10 +627,38 @@ cudaError_t launch_paged_attend(const fa_paged_shape& s, const fa_paged_cache& c
     return e;
   const dim3 grid((unsigned)(P.slots * P.tiles), (unsigned)s.Hkv, (unsigned)s.B);
   paged_rows_kernel<<<grid, PR_THREADS, PR_SMEM, stream>>>(tk, tv, P);
-  if ((e = cudaGetLastError()) != cudaSuccess || P.slots == 1) return e;
-  const long long rows = (long long)s.total_q * s.Hq;
-  paged_join_kernel<<<(unsigned)((rows + 7) / 8), 256, 0, stream>>>(P, PR_ROWS);
-  return cudaGetLastError();
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  float* tile_o = part_o + a.rows_records * FA_HEAD_DIM;
+  float2* tile_ml = part_ml + a.rows_records;
+  if (a.t.tok > 0 &&
+      (e = launch_tiles(s, c, a.t, q, q_stride, scale, window, out, out_stride, lse, tile_o, tile_ml,
+                        PR_ROWS, stream, why)) != cudaSuccess)
+    return e;
+  JoinParams J;
+  memset(&J, 0, sizeof(J));
+  J.p = P.p;
+  J.window = window;
+  J.out = P.out;
+  J.out_stride = out_stride;
+  J.lse = lse;
+  auto join = [&](int chunk, int slots, int tile_rows, int max_rows, int min_rows, const float* o,
+                  const float2* ml) {
+    J.chunk = chunk;
+    J.slots = slots;
+    J.tile_rows = tile_rows;
+    J.max_rows = max_rows;
+    J.min_rows = min_rows;
+    J.part_o = o;
+    J.part_ml = ml;
+    const long long rows = max_rows > 0 ? (long long)s.B * s.Hkv * max_rows : (long long)s.total_q * s.Hq;
+    paged_join_kernel<<<(unsigned)((rows + 7) / 8), 256, 0, stream>>>(J);
+    return cudaGetLastError();
+  };
+  if (P.slots > 1 &&
+      (e = join(P.chunk, P.slots, PR_ROWS, P.max_rows, 0, part_o, part_ml)) != cudaSuccess)
+    return e;
+  if (a.t.slots > 1) e = join(a.t.chunk, a.t.slots, 2 * a.t.tok * P.p.G, 0, PR_ROWS, tile_o, tile_ml);
+  return e;
 }
 
 cudaError_t launch_paged_weights(const fa_paged_shape& s, const fa_paged_cache& c, const void* q,
@@ -615,7 +679,7 @@ cudaError_t launch_paged_weights(const fa_paged_shape& s, const fa_paged_cache& 
   P.weights = weights;
   P.weights_ld = weights_ld;
   P.chunk = rows_chunk(s, 1, sms);
-  P.slots = rows_slots(s, window, P.chunk, (s.max_q < s.total_q ? s.max_q : s.total_q) * P.p.G);
+  P.slots = chunk_slots(s, window, P.chunk, s.max_q < s.total_q ? s.max_q : s.total_q);
   CUtensorMap tk;
   if (!encode_pool(&tk, c.K, s, PR_KEYS)) {
     *why = "cuTensorMapEncodeTiled rejected the pool";

@@ -62,6 +62,31 @@ __device__ __forceinline__ void row_keys(const SeqSpan& s, int G, int window, in
   *lo = window > 0 ? max(0, first - window + 1) : 0;
 }
 
+__device__ __forceinline__ float exp2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// Chunks that the keys of `tokens` neighbouring tokens can touch, in a cache or a window.
+int chunk_slots(const fa_paged_shape& s, int window, int chunk, int tokens);
+
+// Tensor-core tiles of a batch (fa_paged_tc.cu); tok = 0: not used.
+struct TilePlan {
+  int tok, box, tiles, chunk, slots;
+  size_t records;  // partial results
+};
+cudaError_t tile_plan(const fa_paged_shape& s, int window, TilePlan* t);
+// Rows of sequences with more than skip_rows query rows a KV head.
+cudaError_t launch_tiles(const fa_paged_shape& s, const fa_paged_cache& c, const TilePlan& t,
+                         const void* q, int64_t q_stride, float scale, int window, void* out,
+                         int64_t out_stride, float* lse, float* part_o, float2* part_ml,
+                         int skip_rows, cudaStream_t stream, const char** why);
+
 // 2-D map of a pool: rows of 128 bf16 in (page, head, slot) order, boxes of 64 dims x `rows`
 // rows in the 128-byte swizzle.
 bool encode_pool(CUtensorMap* map, const void* pool, const fa_paged_shape& s, int rows);

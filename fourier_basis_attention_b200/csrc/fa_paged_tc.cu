@@ -1,0 +1,510 @@
+// fa_paged_tc.cu -- attention of new tokens over a paged cache on tcgen05, for sequences with
+// more query rows than one 16-row tile (a row = one token and one query head of a KV head).
+//
+// A CTA takes two tiles of 128 rows of one KV head and streams its keys and values in blocks
+// of 128 through a ring of TMA boxes. Per block and tile: S = Q K^T into tensor memory, one
+// thread a row turns S into weights P = exp2(c s - m) (running reference m, running sum l),
+// writes P back over S in bf16, and O += P V reads P from tensor memory. While one tile's
+// threads work on their weights the tensor core works on the other tile.
+//   The reference m follows the running maximum only when it falls behind by 2^8: the weights
+// stay below 256, which costs bf16 and fp32 nothing, and the product m -> O (a pass over O in
+// tensor memory) runs a few times a row instead of once a block.
+//
+// Bound: 4 * 128 flops a (row, key) on the tensor core, and one exp2 (16 a clock and SM): for
+// a 128 x 128 tile 1024 clocks each.
+#include <math.h>
+#include <string.h>
+
+#include "fa_paged.cuh"
+
+namespace fa {
+
+constexpr int PT_KEYS = 128;                  // keys a block
+constexpr int PT_TILE = 128;                  // rows a tile
+constexpr int PT_HALF = 128 * 128;            // 64 dims x 128 rows
+constexpr int PT_BLOCK = 2 * PT_HALF;         // bytes of a block of K, V or Q rows
+constexpr int PT_STAGES = 5;
+constexpr int PT_WARPS = 12;                  // 4 + 4 softmax; producer, MMA and two idle ones
+constexpr int PT_THREADS = PT_WARPS * 32;
+constexpr int PT_SMEM = (2 + PT_STAGES) * PT_BLOCK + 1024;
+constexpr float PT_SLACK = 8.0f;              // log2 by which the maximum may pass m
+
+struct TileParams {
+  PagedBatch p;
+  int window, chunk, slots, tiles;  // keys a chunk, partial results a row, CTA tiles
+  int tok, box;                     // tokens of a 128-row tile, key rows of a TMA box
+  int skip_rows;                    // sequences of at most so many rows are another kernel's
+  float scale_log2;
+  __nv_bfloat16* out;
+  long long out_stride;
+  float* lse;
+  float* part_o;    // [row][slot][128], row = token * Hq + head
+  float2* part_ml;  // [row][slot]
+};
+
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float* a, float* b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(*a), "=f"(*b) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+// Issues the boxes of 128 keys [j0, j0 + 128) of a pool: lanes 0 .. 2 * (128 / box) - 1 hold
+// one box each; `row` is the lane's row in the pool (key_row).
+__device__ __forceinline__ void load_keys(uint8_t* dst, const CUtensorMap* map, uint64_t* bar, int box,
+                                          int row, int lane) {
+  const int n = PT_KEYS / box;
+  if (lane < 2 * n) {
+    const int half = lane >= n, i = lane - half * n;
+    tma_load_2d(dst + half * PT_HALF + i * box * 128, map, bar, 64 * half, row);
+  }
+}
+
+// Row of the pools at which this lane's box of block j0 starts. Boxes without a key of
+// [lo, hi) and entries out of range start behind the pool: the copy fills them with zeros.
+__device__ __forceinline__ int key_row(const PagedBatch& p, int b, int g, int j0, int box, int lo,
+                                       int hi, int lane) {
+  const int n = PT_KEYS / box;
+  const int none = p.num_pages * p.Hkv * p.page;
+  if (lane >= 2 * n) return none;
+  const int j = j0 + (lane % n) * box;
+  if (j >= hi || j + box <= lo) return none;
+  const int pg = page_of(p, b, j);
+  return pg < 0 ? none : (pg * p.Hkv + g) * p.page + j % p.page;
+}
+
+// The sequence of tile x: tiles of T tokens, those of sequence b from q_start[b] / T + b on
+// (ceil(n / T) <= floor((q + n) / T) - floor(q / T) + 1, so the ranges do not overlap).
+__device__ __forceinline__ int tile_sequence(const PagedBatch& p, int x, int T, int lane) {
+  int b = -1;
+  for (int b0 = 0; b0 < p.B; b0 += 32) {
+    const int i = b0 + lane;
+    const int n = __popc(__ballot_sync(0xFFFFFFFFu, i < p.B && p.q_start[i] / T + i <= x));
+    b += n;
+    if (n < 32) break;
+  }
+  return b;
+}
+
+// Waits (at most 0.2 s) for the last copy into each stage, so that none lands after the CTA.
+template <int STAGES>
+__device__ __forceinline__ void drain_ring(uint64_t* full, int issued) {
+  for (int s = 0; s < STAGES; ++s) {
+    if (issued <= s) break;
+    const int last = (issued - 1 - s) / STAGES;  // uses of stage s before the last one
+    const unsigned long long t0 = globaltimer_ns();
+    while (!mbar_try_wait(&full[s], (uint32_t)last & 1u))
+      if (globaltimer_ns() - t0 > 200000000ull) break;
+  }
+}
+
+__global__ void __launch_bounds__(PT_THREADS, 1)
+    paged_tile_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
+                      const __grid_constant__ CUtensorMap tv, const __grid_constant__ TileParams P) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~uintptr_t(1023));
+  uint8_t* ring = smem + 2 * PT_BLOCK;
+  __shared__ uint64_t full[PT_STAGES], empty[PT_STAGES], q_full, s_full[2], p_full[2], drained;
+  __shared__ uint32_t tmem_ptr;
+  __shared__ int abort_word;
+  const PagedBatch& p = P.p;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int g = blockIdx.x % p.Hkv, rest = blockIdx.x / p.Hkv;
+  const int slot = rest % P.slots;
+  const int x = P.tiles - 1 - rest / P.slots;  // late tokens (the most keys) first
+  const int T = 2 * P.tok;
+  const int b = tile_sequence(p, x, T, lane);
+  if (b < 0) return;
+  const SeqSpan s = seq_span(p, b);
+  const int t0 = (x - (s.q0 / T + b)) * T;  // first token of the tile in its sequence
+  if (t0 < 0 || t0 >= s.n || s.n * p.G <= P.skip_rows) return;
+  const int n_tok = min(T, s.n - t0), p0 = s.kv - s.n + t0;  // tokens, position of the first
+  const int two = n_tok > P.tok;
+  const int hi = p0 + n_tok, lo = P.window > 0 ? max(0, p0 - P.window + 1) : 0;
+  const bool single = P.slots == 1;
+  const int c0 = (lo / P.chunk + slot) * P.chunk;
+  const int k_lo = max(lo & ~(PT_KEYS - 1), c0), k_hi = min(hi, c0 + P.chunk);
+  const int nb = k_hi > k_lo ? (k_hi - k_lo + PT_KEYS - 1) / PT_KEYS : 0;
+  if (nb == 0 && !(single || (slot == 0 && hi <= lo))) return;  // the merge skips it
+
+  if (threadIdx.x == 0) {
+    abort_word = 0;
+    for (int i = 0; i < PT_STAGES; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], 1);
+    }
+    mbar_init(&q_full, 1);
+    mbar_init(&drained, 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&s_full[i], 1);
+      mbar_init(&p_full[i], 4);
+    }
+    fence_barrier_init();
+  }
+  if (warp == 9) {
+    tmem_alloc(&tmem_ptr, 512);
+    tmem_relinquish();
+    tc_fence_before();
+  }
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_ptr;  // S / P of tiles 0, 1 at columns 0, 128; O at 256, 384
+  volatile int* abort_flag = &abort_word;
+  // 168 registers a thread at launch: 8 warps take 208, 4 keep 88 (the sum is the same)
+  if (warp >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+  if (warp == 8) {
+    // ------------------------------------------------------------------ producer
+    int issued = 0;
+    if (nb > 0) {
+      const int q_bytes = P.tok * p.G * 128;  // of one 64-dim half of a tile
+      if (lane == 0) {
+        mbar_arrive_expect_tx(&q_full, (uint32_t)(q_bytes * (two ? 4 : 2)));
+        for (int i = 0; i < (two ? 4 : 2); ++i)
+          tma_load_3d(smem + (i >> 1) * PT_BLOCK + (i & 1) * PT_HALF, &tq, &q_full, 64 * (i & 1),
+                      g * p.G, s.q0 + t0 + (i >> 1) * P.tok);
+      }
+      bool ok = true;
+      for (int i = 0; i < nb && ok; ++i) {
+        const int row = key_row(p, b, g, k_lo + i * PT_KEYS, P.box, lo, hi, lane);
+#pragma unroll
+        for (int v = 0; v < 2; ++v) {
+          const int st = issued % PT_STAGES;
+          if (issued >= PT_STAGES)
+            ok = mbar_wait(&empty[st], (uint32_t)(issued / PT_STAGES - 1) & 1u, abort_flag, WD_PAGED | 3u);
+          ok = __all_sync(0xFFFFFFFFu, ok);
+          if (!ok) break;
+          if (lane == 0) mbar_arrive_expect_tx(&full[st], PT_BLOCK);
+          __syncwarp();
+          load_keys(ring + st * PT_BLOCK, v ? &tv : &tk, &full[st], P.box, row, lane);
+          ++issued;
+        }
+      }
+      if (!ok && lane == 0) {
+        drain_ring<PT_STAGES>(full, issued);
+        drain_ring<1>(&q_full, 1);
+      }
+    }
+  } else if (warp == 9) {
+    // ------------------------------------------------------------------ MMA
+    constexpr uint32_t id_s = idesc_bf16_f32(PT_TILE, PT_KEYS, false);
+    constexpr uint32_t id_o = idesc_bf16_f32(PT_TILE, FA_HEAD_DIM, true);
+    const uint32_t q_addr = smem_u32(smem), r_addr = smem_u32(ring);
+    auto scores = [&](int t, int st) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const uint32_t off = (k >> 2) * PT_HALF + (k & 3) * 32;
+        mma_f16(tmem + 128 * t, smem_desc_sw128(q_addr + t * PT_BLOCK + off, 16, 1024),
+                smem_desc_sw128(r_addr + st * PT_BLOCK + off, 16, 1024), id_s, k > 0 ? 1u : 0u);
+      }
+      mma_commit(&s_full[t]);
+    };
+    bool ok = nb > 0 && mbar_wait(&q_full, 0, abort_flag, WD_PAGED | 4u);
+    int c = 0;  // ring use
+    auto use = [&]() {
+      const int st = c % PT_STAGES;
+      ok = ok && mbar_wait(&full[st], (uint32_t)(c / PT_STAGES) & 1u, abort_flag, WD_PAGED | 5u);
+      ok = __all_sync(0xFFFFFFFFu, ok);
+      tc_fence_after();
+      ++c;
+      return st;
+    };
+    if (nb > 0) {
+      const int st = use();
+      if (ok && lane == 0) {
+        scores(0, st);
+        if (two) scores(1, st);
+        mma_commit(&empty[st]);
+      }
+    }
+    for (int i = 0; i < nb && ok; ++i) {
+      const int sv = use();
+      const int j0 = k_lo + i * PT_KEYS;
+      if (ok && (j0 < lo || j0 + PT_KEYS > hi)) {
+        // values of keys outside [lo, hi) may be anything, NaN too: they count as zero
+        uint8_t* v = ring + sv * PT_BLOCK;
+        for (int w = lane; w < PT_KEYS * 16; w += 32) {
+          const int r = w >> 4;
+          if (j0 + r < lo || j0 + r >= hi)
+            *reinterpret_cast<uint4*>(v + ((w >> 3) & 1) * PT_HALF + r * 128 + (w & 7) * 16) =
+                make_uint4(0u, 0u, 0u, 0u);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+      }
+      int sk = -1;
+      for (int t = 0; t < 1 + two && ok; ++t) {
+        ok = mbar_wait(&p_full[t], (uint32_t)i & 1u, abort_flag, WD_PAGED | 6u);
+        ok = __all_sync(0xFFFFFFFFu, ok);
+        if (!ok) break;
+        tc_fence_after();
+        if (lane == 0) {
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            mma_f16_ta(tmem + 256 + 128 * t, tmem + 128 * t + 8 * k,
+                       smem_desc_sw128(r_addr + sv * PT_BLOCK + 2048 * k, PT_HALF, 1024), id_o,
+                       i > 0 || k > 0 ? 1u : 0u);
+          if (t == two) mma_commit(&empty[sv]);
+        }
+        if (i + 1 < nb) {
+          if (t == 0) sk = use();
+          if (!ok) break;
+          if (lane == 0) {
+            scores(t, sk);
+            if (t == two) mma_commit(&empty[sk]);
+          }
+        } else if (lane == 0) {
+          mma_commit(&s_full[t]);  // O is complete
+        }
+      }
+    }
+    if (nb > 0 && !ok && lane == 0) {
+      // tensor memory is released only after every MMA of this CTA has completed
+      mma_commit(&drained);
+      const unsigned long long w0 = globaltimer_ns();
+      while (!mbar_try_wait(&drained, 0))
+        if (globaltimer_ns() - w0 > 200000000ull) break;
+    }
+  }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+  if ((warp >> 2) <= two) {
+    // ------------------------------------------------------------------ softmax, one row a thread
+    const int t = warp >> 2, row = threadIdx.x & 127;
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t ts = tmem + 128 * t + lanes, to = tmem + 256 + 128 * t + lanes;
+    const int tok = t * P.tok + row / p.G;
+    const bool valid = row < P.tok * p.G && tok < n_tok;
+    const int pos = valid ? p0 + tok : -1;
+    const int p_first = p0 + t * P.tok, p_last = min(p_first + P.tok, p0 + n_tok) - 1;
+    const float c = P.scale_log2;
+    float m = -INFINITY, l = 0.0f;
+    bool ok = true;
+    for (int i = 0; i < nb; ++i) {
+      ok = mbar_wait(&s_full[t], (uint32_t)i & 1u, abort_flag, WD_PAGED | 7u);
+      ok = __all_sync(0xFFFFFFFFu, ok);
+      if (!ok) break;
+      tc_fence_after();
+      uint32_t sr[4][32];
+#pragma unroll
+      for (int v = 0; v < 4; ++v) tmem_ld_32x32b_x32(ts + 32 * v, sr[v]);
+      tmem_ld_wait();
+      const int j0 = k_lo + i * PT_KEYS;
+      if (j0 + PT_KEYS > p_first + 1 || (P.window > 0 && j0 <= p_last - P.window)) {
+        const int up = pos - j0, down = P.window > 0 ? pos - P.window - j0 : -1;
+#pragma unroll
+        for (int v = 0; v < 4; ++v)
+#pragma unroll
+          for (int e = 0; e < 32; ++e)
+            if (32 * v + e > up || 32 * v + e <= down) sr[v][e] = 0xFF800000u;
+      }
+      float mx[4];
+#pragma unroll
+      for (int v = 0; v < 4; ++v) {
+        mx[v] = __uint_as_float(sr[v][0]);
+#pragma unroll
+        for (int e = 1; e < 32; ++e) mx[v] = fmaxf(mx[v], __uint_as_float(sr[v][e]));
+      }
+      const float top = c * fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+      if (i == 0) {
+        m = top;
+      } else {
+        const bool behind = valid && top > m + PT_SLACK;
+        if (__any_sync(0xFFFFFFFFu, behind)) {
+          const float m_new = behind ? top : m;
+          const float f = behind ? exp2_approx(m - m_new) : 1.0f;
+          m = m_new;
+          l *= f;
+#pragma unroll 1
+          for (int v = 0; v < 4; ++v) {
+            uint32_t o[32];
+            tmem_ld_32x32b_x32(to + 32 * v, o);
+            tmem_ld_wait();
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(f * __uint_as_float(o[e]));
+            tmem_st_32x32b_x32(to + 32 * v, o);
+          }
+        }
+      }
+      const float base = m == -INFINITY ? 0.0f : m;
+      const uint64_t c2 = pack2(c, c), b2 = pack2(-base, -base);
+      uint64_t sum[2] = {0ull, 0ull};
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        uint32_t w[32];
+#pragma unroll
+        for (int e = 0; e < 32; ++e) {
+          const uint32_t* q = &sr[2 * h + (e >> 4)][2 * (e & 15)];
+          const uint64_t y = fma2(pack2(__uint_as_float(q[0]), __uint_as_float(q[1])), c2, b2);
+          float y0, y1;
+          unpack2(y, &y0, &y1);
+          y0 = exp2_approx(y0);
+          y1 = exp2_approx(y1);
+          sum[e & 1] = add2(sum[e & 1], pack2(y0, y1));
+          w[e] = pack_bf16(y0, y1);
+        }
+        tmem_st_32x32b_x32(ts + 32 * h, w);
+      }
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&p_full[t]);
+      float a0, a1;
+      unpack2(add2(sum[0], sum[1]), &a0, &a1);
+      l += a0 + a1;
+    }
+    if (nb > 0 && ok) {
+      ok = mbar_wait(&s_full[t], (uint32_t)nb & 1u, abort_flag, WD_PAGED | 8u);
+      ok = __all_sync(0xFFFFFFFFu, ok);
+      tc_fence_after();
+    }
+    if (ok) {
+      const long long token = s.q0 + t0 + tok;
+      const int h = g * p.G + row % p.G;
+      const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);
+      const long long rec = (token * p.Hq + h) * P.slots + slot;
+#pragma unroll 1
+      for (int v = 0; v < 4; ++v) {
+        uint32_t o[32];
+        if (nb > 0) {
+          tmem_ld_32x32b_x32(to + 32 * v, o);
+          tmem_ld_wait();
+        } else {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] = 0u;
+        }
+        if (!valid) continue;
+        if (single) {
+          uint4* dst = reinterpret_cast<uint4*>(P.out + token * P.out_stride + h * FA_HEAD_DIM + 32 * v);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            uint32_t w[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+              w[u] = pack_bf16(inv * __uint_as_float(o[8 * e + 2 * u]),
+                               inv * __uint_as_float(o[8 * e + 2 * u + 1]));
+            dst[e] = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+        } else {
+          uint4* dst = reinterpret_cast<uint4*>(P.part_o + rec * FA_HEAD_DIM + 32 * v);
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            dst[e] = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+        }
+      }
+      if (valid) {
+        if (!single) P.part_ml[rec] = make_float2(m, l);
+        else if (P.lse) P.lse[token * p.Hq + h] = 0.693147180559945309f * (m + log2f(l));
+      }
+    }
+  }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 9) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+FA_WATCHDOG_READER(read_watchdog_paged_tc)
+
+// ------------------------------------------------------------------------- host side
+bool encode_queries(CUtensorMap* map, const void* q, const fa_paged_shape& s, int64_t stride, int tok) {
+  const auto encode = reinterpret_cast<decltype(&cuTensorMapEncodeTiled)>(tensor_map_encoder());
+  if (!encode) return false;
+  const int G = s.Hq / s.Hkv;
+  cuuint64_t dims[3] = {FA_HEAD_DIM, (cuuint64_t)s.Hq, (cuuint64_t)s.total_q};
+  cuuint64_t strides[2] = {FA_HEAD_DIM * 2, (cuuint64_t)stride * 2};
+  cuuint32_t box[3] = {64, (cuuint32_t)G, (cuuint32_t)tok};
+  cuuint32_t estr[3] = {1, 1, 1};
+  return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(q), dims, strides, box,
+                estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Key rows of a TMA box: the largest power of two, at most a block, that divides a page (so
+// that no box crosses its end); a whole block where a sequence has one page.
+int key_box(const fa_paged_shape& s) {
+  if (s.max_kv <= s.page_size) return PT_KEYS;
+  int box = 16;
+  while (box < PT_KEYS && s.page_size % (2 * box) == 0) box *= 2;
+  return box;
+}
+
+// Tiles are used where some sequence may have more rows than one 16-row tile and the heads of
+// a token fit a 128-row tile. Keys are split when the tiles of the batch leave SMs idle: into
+// chunks of equal length (multiples of a block, at least 4 blocks) that fill one wave.
+cudaError_t tile_plan(const fa_paged_shape& s, int window, TilePlan* t) {
+  memset(t, 0, sizeof(*t));
+  const int G = s.Hq / s.Hkv;
+  const long long max_q = s.max_q < s.total_q ? s.max_q : s.total_q;
+  if (G > PT_TILE || max_q * G <= 16) return cudaSuccess;
+  int sms = 148;
+  cudaError_t e = device_sm_count(&sms);
+  if (e != cudaSuccess) return e;
+  t->tok = PT_TILE / G;
+  t->box = key_box(s);
+  const int T = 2 * t->tok;
+  t->tiles = s.total_q / T + s.B;
+  const long long units = (long long)((s.total_q + T - 1) / T) * s.Hkv;
+  const long long want = units < sms ? sms / units : 1;
+  long long c = (s.max_kv + want - 1) / want;
+  c = (c + PT_KEYS - 1) / PT_KEYS * PT_KEYS;
+  t->chunk = (int)(c < 4 * PT_KEYS ? 4 * PT_KEYS : c);
+  t->slots = chunk_slots(s, window, t->chunk, T);
+  t->records = t->slots == 1 ? 0 : (size_t)s.total_q * s.Hq * t->slots;
+  return cudaSuccess;
+}
+
+cudaError_t launch_tiles(const fa_paged_shape& s, const fa_paged_cache& c, const TilePlan& t,
+                         const void* q, int64_t q_stride, float scale, int window, void* out,
+                         int64_t out_stride, float* lse, float* part_o, float2* part_ml,
+                         int skip_rows, cudaStream_t stream, const char** why) {
+  TileParams P;
+  memset(&P, 0, sizeof(P));
+  P.p = paged_batch(s, c);
+  P.window = window;
+  P.chunk = t.chunk;
+  P.slots = t.slots;
+  P.tiles = t.tiles;
+  P.tok = t.tok;
+  P.box = t.box;
+  P.skip_rows = skip_rows;
+  P.scale_log2 = scale * 1.44269504088896341f;
+  P.out = static_cast<__nv_bfloat16*>(out);
+  P.out_stride = out_stride;
+  P.lse = lse;
+  P.part_o = part_o;
+  P.part_ml = part_ml;
+  CUtensorMap tq, tk, tv;
+  if (!encode_pool(&tk, c.K, s, t.box) || !encode_pool(&tv, c.V, s, t.box)) {
+    *why = "cuTensorMapEncodeTiled rejected the pools";
+    return cudaErrorInvalidValue;
+  }
+  if (!encode_queries(&tq, q, s, q_stride, t.tok)) {
+    *why = "cuTensorMapEncodeTiled rejected q";
+    return cudaErrorInvalidValue;
+  }
+  const void* fn = reinterpret_cast<const void*>(paged_tile_kernel);
+  cudaError_t e = raise_smem_limit(fn, PT_SMEM);
+  if (e != cudaSuccess) return e;
+  const long long ctas = (long long)t.tiles * t.slots * s.Hkv;
+  paged_tile_kernel<<<(unsigned)ctas, PT_THREADS, PT_SMEM, stream>>>(tq, tk, tv, P);
+  return cudaGetLastError();
+}
+
+}  // namespace fa
