@@ -421,7 +421,7 @@ __global__ void __launch_bounds__(PR_THREADS, 2)
   const int g = blockIdx.y, b = blockIdx.z;
   const SeqSpan s = seq_span(p, b);
   const int n_rows = s.n * p.G;
-  if (n_rows <= 0) return;
+  if (n_rows <= 0 || (P.max_rows > 0 && n_rows > P.max_rows)) return;
   int lo, hi;
   row_keys(s, p.G, P.window, 0, n_rows, &lo, &hi);
   const int c0 = (lo / P.chunk + blockIdx.x) * P.chunk;
@@ -678,8 +678,12 @@ cudaError_t launch_paged_weights(const fa_paged_shape& s, const fa_paged_cache& 
   P.lse = const_cast<float*>(lse);
   P.weights = weights;
   P.weights_ld = weights_ld;
+  // tensor-core tiles as in attend_plan
+  const long long max_q = s.max_q < s.total_q ? s.max_q : s.total_q;
+  const bool tiles = P.p.G <= 128 && max_q * P.p.G > PR_ROWS;
+  P.max_rows = tiles ? PR_ROWS : 0;
   P.chunk = rows_chunk(s, 1, sms);
-  P.slots = chunk_slots(s, window, P.chunk, s.max_q < s.total_q ? s.max_q : s.total_q);
+  P.slots = chunk_slots(s, window, P.chunk, tiles ? PR_ROWS : (int)max_q);
   CUtensorMap tk;
   if (!encode_pool(&tk, c.K, s, PR_KEYS)) {
     *why = "cuTensorMapEncodeTiled rejected the pool";
@@ -689,7 +693,9 @@ cudaError_t launch_paged_weights(const fa_paged_shape& s, const fa_paged_cache& 
   if ((e = raise_smem_limit(fn, PR_SMEM)) != cudaSuccess) return e;
   const dim3 grid((unsigned)P.slots, (unsigned)s.Hkv, (unsigned)s.B);
   paged_weights_rows_kernel<<<grid, PR_THREADS, PR_SMEM, stream>>>(tk, P);
-  return cudaGetLastError();
+  if ((e = cudaGetLastError()) != cudaSuccess || !tiles) return e;
+  return launch_weight_tiles(s, c, q, q_stride, scale, window, lse, weights, weights_ld, PR_ROWS,
+                             stream, why);
 }
 
 }  // namespace fa

@@ -87,6 +87,11 @@ cudaError_t launch_tiles(const fa_paged_shape& s, const fa_paged_cache& c, const
                          int64_t out_stride, float* lse, float* part_o, float2* part_ml,
                          int skip_rows, cudaStream_t stream, const char** why);
 
+cudaError_t launch_weight_tiles(const fa_paged_shape& s, const fa_paged_cache& c, const void* q,
+                                int64_t q_stride, float scale, int window, const float* lse,
+                                float* weights, int64_t weights_ld, int skip_rows,
+                                cudaStream_t stream, const char** why);
+
 // 2-D map of a pool: rows of 128 bf16 in (page, head, slot) order, boxes of 64 dims x `rows`
 // rows in the 128-byte swizzle.
 bool encode_pool(CUtensorMap* map, const void* pool, const fa_paged_shape& s, int rows);

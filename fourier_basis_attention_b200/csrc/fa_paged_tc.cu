@@ -420,6 +420,240 @@ __global__ void __launch_bounds__(PT_THREADS, 1)
   }
 }
 
+// Weights that keys gather: w_j += sum_rows exp2(c s_rj - log2 e lse_r). A CTA keeps 256 keys
+// (two tiles) and streams the query rows that see them in blocks of 128, as S^T = K Q^T: a
+// thread owns a key (a lane of tensor memory) and sums along its columns, so that nothing is
+// reduced across threads and a key's sum is taken in one order. Scores are double-buffered:
+// the tensor core writes one buffer while the other is summed. Bound: 2 * 128 flops a (row,
+// key) against one exp2: 512 and 1024 clocks for a 128 x 128 tile.
+constexpr int PV_STAGES = 4;
+constexpr int PV_KEYS = 2 * PT_TILE;
+constexpr int PV_SMEM = (2 + PV_STAGES) * PT_BLOCK + 1024;
+
+struct WeightParams {
+  PagedBatch p;
+  int window, tok, box, skip_rows;
+  float scale_log2;
+  const float* lse;
+  float* weights;
+  long long weights_ld;
+};
+
+__global__ void __launch_bounds__(PT_THREADS, 1)
+    paged_weights_tile_kernel(const __grid_constant__ CUtensorMap tq,
+                              const __grid_constant__ CUtensorMap tk,
+                              const __grid_constant__ WeightParams P) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~uintptr_t(1023));
+  uint8_t* ring = smem + 2 * PT_BLOCK;
+  __shared__ uint64_t full[PV_STAGES], empty[PV_STAGES], k_full, s_full[4], s_empty[4], drained;
+  __shared__ __align__(16) float minus_lse[PV_STAGES][PT_TILE];
+  __shared__ uint32_t tmem_ptr;
+  __shared__ int abort_word;
+  const PagedBatch& p = P.p;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int g = blockIdx.y, b = blockIdx.z;
+  const SeqSpan s = seq_span(p, b);
+  if (s.n * p.G <= P.skip_rows || s.kv <= 0) return;
+  const int p0 = s.kv - s.n;  // position of the first new token
+  const int hi = s.kv, lo = P.window > 0 ? max(0, p0 - P.window + 1) : 0;
+  const int j0 = (lo / PV_KEYS + (int)blockIdx.x) * PV_KEYS;
+  if (j0 >= hi) return;
+  const int two = j0 + PT_TILE < hi;
+  // tokens that see a key of the tiles, in blocks of P.tok
+  const int i0 = max(0, j0 - p0);
+  const int i1 = P.window > 0 ? min(s.n, min(j0 + PV_KEYS, hi) - 1 + P.window - p0) : s.n;
+  const int blk0 = i0 / P.tok, nb = (i1 + P.tok - 1) / P.tok - blk0;
+  if (nb <= 0) return;
+
+  if (threadIdx.x == 0) {
+    abort_word = 0;
+    for (int i = 0; i < PV_STAGES; ++i) {
+      mbar_init(&full[i], 2);
+      mbar_init(&empty[i], 1 + 4 * (1 + two));
+    }
+    mbar_init(&k_full, 1);
+    mbar_init(&drained, 1);
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(&s_full[i], 1);
+      mbar_init(&s_empty[i], 4);
+    }
+    fence_barrier_init();
+  }
+  if (warp == 9) {
+    tmem_alloc(&tmem_ptr, 512);
+    tmem_relinquish();
+    tc_fence_before();
+  }
+  // rows of the blocks that no box fills (128 is not a multiple of G) are zero
+  for (int w = threadIdx.x; w < PV_STAGES * 2 * (PT_TILE - P.tok * p.G) * 8; w += PT_THREADS) {
+    const int pad = PT_TILE - P.tok * p.G, r = PT_TILE - 1 - w / 8 % pad, h = w / 8 / pad;
+    *reinterpret_cast<uint4*>(ring + h * PT_HALF + r * 128 + (w & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+  }
+  fence_proxy_async_smem();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_ptr;  // scores of tile t, buffer u at columns 128 (2 t + u)
+  volatile int* abort_flag = &abort_word;
+
+  if (warp >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    if (warp == 8) {
+      // ---------------------------------------------------------------- producer
+      bool ok = true;
+      int issued = 0;
+      for (int t = 0; t < 1 + two; ++t) {
+        const int row = key_row(p, b, g, j0 + t * PT_TILE, P.box, lo, hi, lane);
+        if (t == 0 && lane == 0) mbar_arrive_expect_tx(&k_full, PT_BLOCK * (1 + two));
+        __syncwarp();
+        load_keys(smem + t * PT_BLOCK, &tk, &k_full, P.box, row, lane);
+      }
+      for (int i = 0; i < nb && ok; ++i) {
+        const int st = i % PV_STAGES;
+        if (i >= PV_STAGES)
+          ok = mbar_wait(&empty[st], (uint32_t)(i / PV_STAGES - 1) & 1u, abort_flag, WD_PAGED | 9u);
+        ok = __all_sync(0xFFFFFFFFu, ok);
+        if (!ok) break;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(&full[st], (uint32_t)(P.tok * p.G * 256));
+          for (int h = 0; h < 2; ++h)
+            tma_load_3d(ring + st * PT_BLOCK + h * PT_HALF, &tq, &full[st], 64 * h, g * p.G,
+                        s.q0 + (blk0 + i) * P.tok);
+        }
+        ++issued;
+      }
+      if (!ok && lane == 0) {
+        drain_ring<PV_STAGES>(full, issued);
+        drain_ring<1>(&k_full, 1);
+      }
+    } else if (warp == 9) {
+      // ---------------------------------------------------------------- MMA
+      constexpr uint32_t id = idesc_bf16_f32(PT_TILE, PT_TILE, false);
+      const uint32_t k_addr = smem_u32(smem), r_addr = smem_u32(ring);
+      bool ok = mbar_wait(&k_full, 0, abort_flag, WD_PAGED | 10u);
+      for (int i = 0; i < nb; ++i) {
+        const int st = i % PV_STAGES, u = i & 1;
+        ok = ok && mbar_wait(&full[st], (uint32_t)(i / PV_STAGES) & 1u, abort_flag, WD_PAGED | 11u);
+        for (int t = 0; t < 1 + two; ++t) {
+          if (i >= 2)
+            ok = ok && mbar_wait(&s_empty[2 * t + u], (uint32_t)(i / 2 - 1) & 1u, abort_flag, WD_PAGED | 12u);
+          ok = __all_sync(0xFFFFFFFFu, ok);
+          if (!ok) break;
+          tc_fence_after();
+          if (lane == 0) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              const uint32_t off = (k >> 2) * PT_HALF + (k & 3) * 32;
+              mma_f16(tmem + 128 * (2 * t + u), smem_desc_sw128(k_addr + t * PT_BLOCK + off, 16, 1024),
+                      smem_desc_sw128(r_addr + st * PT_BLOCK + off, 16, 1024), id, k > 0 ? 1u : 0u);
+            }
+            mma_commit(&s_full[2 * t + u]);
+            if (t == two) mma_commit(&empty[st]);
+          }
+        }
+        if (!ok) break;
+      }
+      if (!ok && lane == 0) {
+        mma_commit(&drained);
+        const unsigned long long w0 = globaltimer_ns();
+        while (!mbar_try_wait(&drained, 0))
+          if (globaltimer_ns() - w0 > 200000000ull) break;
+      }
+    } else if (warp == 10) {
+      // ---------------------------------------------------------------- log-sum-exp of the rows
+      for (int i = 0; i < nb; ++i) {
+        const int st = i % PV_STAGES;
+        float4 v;
+        float* e = &v.x;
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          const int col = 4 * lane + x, tok = (blk0 + i) * P.tok + col / p.G;
+          e[x] = -INFINITY;  // columns without a row, and rows that see no key, add nothing
+          if (col < P.tok * p.G && tok < s.n) {
+            const float l = P.lse[(long long)(s.q0 + tok) * p.Hq + g * p.G + col % p.G];
+            if (l != -INFINITY) e[x] = -1.44269504088896341f * l;
+          }
+        }
+        bool ok = true;
+        if (i >= PV_STAGES)
+          ok = mbar_wait(&empty[st], (uint32_t)(i / PV_STAGES - 1) & 1u, abort_flag, WD_PAGED | 13u);
+        if (!__all_sync(0xFFFFFFFFu, ok)) break;
+        *reinterpret_cast<float4*>(&minus_lse[st][4 * lane]) = v;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&full[st]);
+      }
+    }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+    if ((warp >> 2) <= two) {
+      // ---------------------------------------------------------------- sums, one key a thread
+      const int t = warp >> 2;
+      const int j = j0 + threadIdx.x, jt = j0 + t * PT_TILE;
+      const uint32_t ts = tmem + 256 * t + ((uint32_t)((warp & 3) * 32) << 16);
+      const uint64_t c2 = pack2(P.scale_log2, P.scale_log2);
+      uint64_t sum[2] = {0ull, 0ull};
+      bool ok = true;
+      for (int i = 0; i < nb; ++i) {
+        const int st = i % PV_STAGES, u = i & 1;
+        ok = mbar_wait(&full[st], (uint32_t)(i / PV_STAGES) & 1u, abort_flag, WD_PAGED | 14u) &&
+             mbar_wait(&s_full[2 * t + u], (uint32_t)(i / 2) & 1u, abort_flag, WD_PAGED | 15u);
+        ok = __all_sync(0xFFFFFFFFu, ok);
+        if (!ok) break;
+        tc_fence_after();
+        uint32_t sr[4][32];
+#pragma unroll
+        for (int v = 0; v < 4; ++v) tmem_ld_32x32b_x32(ts + 128 * u + 32 * v, sr[v]);
+        tmem_ld_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&s_empty[2 * t + u]);
+        // columns [first, last) see the key: tokens from position j on, below j + window
+        const int tok0 = (blk0 + i) * P.tok, pb = p0 + tok0, left = s.n - tok0;
+        const bool edge = jt + PT_TILE - 1 > pb || left < P.tok ||
+                          (P.window > 0 && pb + P.tok > jt + P.window);
+        if (edge) {
+          const int first = min(max(j - pb, 0), P.tok) * p.G;
+          int end = min(left, P.tok);
+          if (P.window > 0) end = min(end, max(0, j + P.window - pb));
+          const int last = end * p.G;
+#pragma unroll
+          for (int v = 0; v < 4; ++v)
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (32 * v + e < first || 32 * v + e >= last) sr[v][e] = 0xFF800000u;
+        }
+        const float4* nl = reinterpret_cast<const float4*>(minus_lse[st]);
+#pragma unroll
+        for (int e = 0; e < 32; ++e) {
+          const float4 w = nl[e];
+          const uint32_t* q = &sr[e >> 3][4 * (e & 7)];
+          const uint64_t ya = fma2(pack2(__uint_as_float(q[0]), __uint_as_float(q[1])), c2, pack2(w.x, w.y));
+          const uint64_t yb = fma2(pack2(__uint_as_float(q[2]), __uint_as_float(q[3])), c2, pack2(w.z, w.w));
+          float a0, a1, b0, b1;
+          unpack2(ya, &a0, &a1);
+          unpack2(yb, &b0, &b1);
+          sum[0] = add2(sum[0], pack2(exp2_approx(a0), exp2_approx(a1)));
+          sum[1] = add2(sum[1], pack2(exp2_approx(b0), exp2_approx(b1)));
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&empty[st]);
+      }
+      if (ok && j >= lo && j < hi) {
+        float a0, a1;
+        unpack2(add2(sum[0], sum[1]), &a0, &a1);
+        P.weights[((long long)b * p.Hkv + g) * P.weights_ld + j] += a0 + a1;
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 9) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
 FA_WATCHDOG_READER(read_watchdog_paged_tc)
 
 // ------------------------------------------------------------------------- host side
@@ -504,6 +738,35 @@ cudaError_t launch_tiles(const fa_paged_shape& s, const fa_paged_cache& c, const
   if (e != cudaSuccess) return e;
   const long long ctas = (long long)t.tiles * t.slots * s.Hkv;
   paged_tile_kernel<<<(unsigned)ctas, PT_THREADS, PT_SMEM, stream>>>(tq, tk, tv, P);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_weight_tiles(const fa_paged_shape& s, const fa_paged_cache& c, const void* q,
+                                int64_t q_stride, float scale, int window, const float* lse,
+                                float* weights, int64_t weights_ld, int skip_rows,
+                                cudaStream_t stream, const char** why) {
+  WeightParams P;
+  memset(&P, 0, sizeof(P));
+  P.p = paged_batch(s, c);
+  P.window = window;
+  P.tok = PT_TILE / P.p.G;
+  P.box = key_box(s);
+  P.skip_rows = skip_rows;
+  P.scale_log2 = scale * 1.44269504088896341f;
+  P.lse = lse;
+  P.weights = weights;
+  P.weights_ld = weights_ld;
+  CUtensorMap tq, tk;
+  if (!encode_pool(&tk, c.K, s, P.box) || !encode_queries(&tq, q, s, q_stride, P.tok)) {
+    *why = "cuTensorMapEncodeTiled rejected the pool or q";
+    return cudaErrorInvalidValue;
+  }
+  const void* fn = reinterpret_cast<const void*>(paged_weights_tile_kernel);
+  cudaError_t e = raise_smem_limit(fn, PV_SMEM);
+  if (e != cudaSuccess) return e;
+  const int max_q = s.max_q < s.total_q ? s.max_q : s.total_q;
+  const dim3 grid((unsigned)chunk_slots(s, window, PV_KEYS, max_q), (unsigned)s.Hkv, (unsigned)s.B);
+  paged_weights_tile_kernel<<<grid, PT_THREADS, PV_SMEM, stream>>>(tq, tk, P);
   return cudaGetLastError();
 }
 
