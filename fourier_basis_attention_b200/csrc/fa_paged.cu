@@ -22,14 +22,14 @@ constexpr int PR_KEYS = 16;     // keys a block
 constexpr int PR_WARPS = 4;
 constexpr int PR_THREADS = PR_WARPS * 32;
 constexpr int PR_BOX = PR_KEYS * 128;       // 64 dims x 16 keys
-constexpr int PR_STAGES = 3;
+constexpr int PR_STAGES = 2;
 constexpr int PR_STAGE = 4 * PR_BOX;        // K and V, two boxes each
-constexpr int PW_STAGES = 6;
+constexpr int PW_STAGES = 3;
 constexpr int PW_STAGE = 2 * PR_BOX;        // K only
 constexpr int PR_OLD = FA_HEAD_DIM + 4;     // fp32 row of the merge buffer
 constexpr int PR_RING = PR_WARPS * PR_STAGES * PR_STAGE;
 constexpr int PR_SMEM = PR_RING + 1024;
-static_assert(PR_WARPS * PW_STAGES * PW_STAGE <= PR_RING, "one shared-memory size");
+constexpr int PW_SMEM = PR_WARPS * PW_STAGES * PW_STAGE + 1024;
 static_assert(PR_WARPS * PR_ROWS * (PR_OLD + 2) * 4 <= PR_RING, "merge buffers fit");
 
 struct RowsParams {
@@ -120,12 +120,15 @@ struct BlockRing {
   const PagedBatch* p;
   int b, g, k0, n;  // first key of the warp, number of its blocks
 
-  __device__ void issue(int i) const {
-    const int s = i % STAGES, j = k0 + i * PR_WARPS * PR_KEYS;
+  // Row of the pools at which block i starts. An entry out of range lies behind the pool: the
+  // copy fills the box with zeros.
+  __device__ int row_of(int i) const {
+    const int j = k0 + i * PR_WARPS * PR_KEYS;
     const int pg = page_of(*p, b, j);
-    // an entry out of range reads behind the pool: the copy fills the box with zeros
-    const int row = pg < 0 ? p->num_pages * p->Hkv * p->page
-                           : (pg * p->Hkv + g) * p->page + j % p->page;
+    return pg < 0 ? p->num_pages * p->Hkv * p->page : (pg * p->Hkv + g) * p->page + j % p->page;
+  }
+  __device__ void issue(int i, int row) const {
+    const int s = i % STAGES;
     uint8_t* dst = buf + s * BYTES;
     mbar_arrive_expect_tx(&full[s], BYTES);
     tma_load_2d(dst, tk, &full[s], 0, row);
@@ -145,7 +148,7 @@ struct BlockRing {
   }
 };
 
-__global__ void __launch_bounds__(PR_THREADS, 2)
+__global__ void __launch_bounds__(PR_THREADS, 3)
     paged_rows_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
                       const __grid_constant__ RowsParams P) {
   extern __shared__ uint8_t smem_raw[];
@@ -188,7 +191,7 @@ __global__ void __launch_bounds__(PR_THREADS, 2)
   const int left = k_hi - ring.k0;
   ring.n = left > 0 ? (left + PR_WARPS * PR_KEYS - 1) / (PR_WARPS * PR_KEYS) : 0;
   if (lane == 0)
-    for (int i = 0; i < min(PR_STAGES, ring.n); ++i) ring.issue(i);
+    for (int i = 0; i < min(PR_STAGES, ring.n); ++i) ring.issue(i, ring.row_of(i));
 
   uint32_t qf[8][4];
   load_q(P, s, g, r0, rows, lane, qf);
@@ -207,6 +210,8 @@ __global__ void __launch_bounds__(PR_THREADS, 2)
 
   for (int i = 0; i < ring.n; ++i) {
     const int st = i % PR_STAGES;
+    int next = 0;  // looked up while this block is on its way
+    if (lane == 0 && i + PR_STAGES < ring.n) next = ring.row_of(i + PR_STAGES);
     const bool ok = mbar_wait(&ring.full[st], (uint32_t)(i / PR_STAGES) & 1u, abort_flag, WD_PAGED | 1u);
     if (!__all_sync(0xFFFFFFFFu, ok)) {
       if (lane == 0) ring.drain(i);
@@ -282,7 +287,7 @@ __global__ void __launch_bounds__(PR_THREADS, 2)
       mma_16816(o[n + 1], pf, v[2], v[3]);
     }
     __syncwarp();
-    if (lane == 0 && i + PR_STAGES < ring.n) ring.issue(i + PR_STAGES);
+    if (lane == 0 && i + PR_STAGES < ring.n) ring.issue(i + PR_STAGES, next);
   }
 #pragma unroll
   for (int u = 0; u < 2; ++u) {
@@ -408,7 +413,7 @@ __global__ void __launch_bounds__(256) paged_join_kernel(const __grid_constant__
 
 // Weights: a warp owns its blocks of 16 keys and runs over every tile of query rows that sees
 // them, so a key's sum is taken by one warp in one order.
-__global__ void __launch_bounds__(PR_THREADS, 2)
+__global__ void __launch_bounds__(PR_THREADS, 4)
     paged_weights_rows_kernel(const __grid_constant__ CUtensorMap tk,
                               const __grid_constant__ RowsParams P) {
   extern __shared__ uint8_t smem_raw[];
@@ -445,14 +450,26 @@ __global__ void __launch_bounds__(PR_THREADS, 2)
   const int left = k_hi - ring.k0;
   ring.n = left > 0 ? (left + PR_WARPS * PR_KEYS - 1) / (PR_WARPS * PR_KEYS) : 0;
   if (lane == 0)
-    for (int i = 0; i < min(PW_STAGES, ring.n); ++i) ring.issue(i);
+    for (int i = 0; i < min(PW_STAGES, ring.n); ++i) ring.issue(i, ring.row_of(i));
 
   uint32_t qf[8][4];
   float ls[2];
   int pos[2];
   int have = -1;
+  // after the sums are spread over the lanes, a lane holds this key of a block
+  const int key = 8 * (lane >> 4) + 2 * (lane & 3) + ((lane >> 3) & 1);
+  float* w = P.weights + ((long long)b * p.Hkv + g) * P.weights_ld;
+  auto old_weight = [&](int i) {
+    const int j = ring.k0 + i * PR_WARPS * PR_KEYS + key;
+    return i < ring.n && !(lane & 4) && j >= lo && j < hi ? w[j] : 0.0f;
+  };
+  float old = old_weight(0);
   for (int i = 0; i < ring.n; ++i) {
     const int st = i % PW_STAGES;
+    // the next loads that the block's end needs, a block ahead
+    const float old_next = old_weight(i + 1);
+    int next = 0;
+    if (lane == 0 && i + PW_STAGES < ring.n) next = ring.row_of(i + PW_STAGES);
     const bool ok = mbar_wait(&ring.full[st], (uint32_t)(i / PW_STAGES) & 1u, &abort_word, WD_PAGED | 2u);
     if (!__all_sync(0xFFFFFFFFu, ok)) {
       if (lane == 0) ring.drain(i);
@@ -492,20 +509,19 @@ __global__ void __launch_bounds__(PR_THREADS, 2)
           if (seen) sum[2 * n + (v & 1)] += exp2_approx(fmaf(sc[n][v], P.scale_log2, -ls[v >> 1]));
         }
     }
-#pragma unroll
-    for (int v = 0; v < 4; ++v)
-#pragma unroll
-      for (int x = 4; x < 32; x <<= 1) sum[v] += __shfl_xor_sync(0xFFFFFFFFu, sum[v], x);
-    if (lane < 4) {
-      float* w = P.weights + ((long long)b * p.Hkv + g) * P.weights_ld;
-#pragma unroll
-      for (int v = 0; v < 4; ++v) {
-        const int j = j0 + 2 * lane + (v & 1) + 8 * (v >> 1);
-        if (j >= lo && j < hi) w[j] += sum[v];
-      }
-    }
     __syncwarp();
-    if (lane == 0 && i + PW_STAGES < ring.n) ring.issue(i + PW_STAGES);
+    if (lane == 0 && i + PW_STAGES < ring.n) ring.issue(i + PW_STAGES, next);
+    // sum over the 8 lanes of a key, halving what a lane holds at each exchange
+    const bool n1 = lane & 16, odd = lane & 8;
+    float a = n1 ? sum[2] : sum[0], c = n1 ? sum[3] : sum[1];
+    a += __shfl_xor_sync(0xFFFFFFFFu, n1 ? sum[0] : sum[2], 16);
+    c += __shfl_xor_sync(0xFFFFFFFFu, n1 ? sum[1] : sum[3], 16);
+    float total = odd ? c : a;
+    total += __shfl_xor_sync(0xFFFFFFFFu, odd ? a : c, 8);
+    total += __shfl_xor_sync(0xFFFFFFFFu, total, 4);
+    const int j = j0 + key;
+    if (!(lane & 4) && j >= lo && j < hi) w[j] = old + total;
+    old = old_next;
   }
 }
 
@@ -543,12 +559,14 @@ bool encode_pool(CUtensorMap* map, const void* pool, const fa_paged_shape& s, in
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Keys a chunk: two CTAs to an SM (what shared memory holds) for the widest batch the shape
-// allows, in multiples of 64 keys, at least 256 (below that the merge costs more than the
-// chunk's own read).
-static int rows_chunk(const fa_paged_shape& s, int tiles, int sms) {
+// Keys a chunk, in multiples of 64: `ctas` CTAs for the longest batch the shape allows, but at
+// least 256 keys (below that the merge costs more than the chunk's own read). Real batches are
+// shorter and ragged, so the targets are many CTAs an SM: 64 sequences of up to 16384 tokens
+// decode in 452, 366, 345, 356 us for 2, 8, 32, 64 a SM (3 are resident); key weights of 32
+// sequences of up to 8192 take 68, 63, 63, 68 us for 8, 16, 32, 64 (4 are resident).
+static int rows_chunk(const fa_paged_shape& s, int tiles, int ctas) {
   const long long units = (long long)s.B * s.Hkv * tiles;
-  const long long want = (2LL * sms + units - 1) / units;
+  const long long want = (ctas + units - 1) / units;
   long long c = (s.max_kv + want - 1) / want;
   c = (c + 63) / 64 * 64;
   return (int)(c < 256 ? 256 : c);
@@ -583,7 +601,7 @@ static cudaError_t attend_plan(const fa_paged_shape& s, int window, AttendPlan* 
   memset(P, 0, sizeof(*P));
   P->max_rows = a->t.tok > 0 || rows <= PR_ROWS ? PR_ROWS : 0;
   P->tiles = P->max_rows > 0 ? 1 : (int)((rows + PR_ROWS - 1) / PR_ROWS);
-  P->chunk = rows_chunk(s, P->tiles, sms);
+  P->chunk = rows_chunk(s, P->tiles, 32 * sms);
   P->slots = chunk_slots(s, window, P->chunk, (PR_ROWS + G - 1) / G);
   P->window = window;
   a->rows_records = 0;
@@ -682,7 +700,7 @@ cudaError_t launch_paged_weights(const fa_paged_shape& s, const fa_paged_cache& 
   const long long max_q = s.max_q < s.total_q ? s.max_q : s.total_q;
   const bool tiles = P.p.G <= 128 && max_q * P.p.G > PR_ROWS;
   P.max_rows = tiles ? PR_ROWS : 0;
-  P.chunk = rows_chunk(s, 1, sms);
+  P.chunk = rows_chunk(s, 1, 16 * sms);
   P.slots = chunk_slots(s, window, P.chunk, tiles ? PR_ROWS : (int)max_q);
   CUtensorMap tk;
   if (!encode_pool(&tk, c.K, s, PR_KEYS)) {
@@ -690,9 +708,9 @@ cudaError_t launch_paged_weights(const fa_paged_shape& s, const fa_paged_cache& 
     return cudaErrorInvalidValue;
   }
   const void* fn = reinterpret_cast<const void*>(paged_weights_rows_kernel);
-  if ((e = raise_smem_limit(fn, PR_SMEM)) != cudaSuccess) return e;
+  if ((e = raise_smem_limit(fn, PW_SMEM)) != cudaSuccess) return e;
   const dim3 grid((unsigned)P.slots, (unsigned)s.Hkv, (unsigned)s.B);
-  paged_weights_rows_kernel<<<grid, PR_THREADS, PR_SMEM, stream>>>(tk, P);
+  paged_weights_rows_kernel<<<grid, PR_THREADS, PW_SMEM, stream>>>(tk, P);
   if ((e = cudaGetLastError()) != cudaSuccess || !tiles) return e;
   return launch_weight_tiles(s, c, q, q_stride, scale, window, lse, weights, weights_ld, PR_ROWS,
                              stream, why);
