@@ -9,6 +9,9 @@ Tolerances (u16 = 2^-8, u32 = 2^-24: half steps of bf16 and fp32; A: the largest
 - rotation: cos and sin are off by 2 u32 + pi 2^-26, products and the sum by u32 each.
 """
 import ctypes
+import os
+import subprocess
+import sys
 
 import numpy as np
 import pytest
@@ -18,6 +21,7 @@ import fourier_basis_attention_b200 as fa
 from oracle import paged_oracle as po
 
 pytestmark = pytest.mark.gpu
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 D = 128
 U16, U32 = 2.0 ** -8, 2.0 ** -24
 BF = torch.bfloat16
@@ -484,6 +488,22 @@ def test_evict(kvs, page, keep, sink, recent, dst_page, kind):
         w = rng.choice(np.array([0.0, -0.0, np.nan, np.inf, -np.inf, 1e-42, -1e-42, 1.0, -2.0],
                                 dtype=np.float32), (B, 2, ld))
     check_evict(st, torch.tensor(w).cuda(), keep, sink, recent, dst_page, with_weights=kind != "ties")
+
+
+def test_first_call_of_a_process_holds_8191_weights():
+    """Dynamic and static shared memory together pass 48 KB before the limit was ever raised."""
+    code = ("import sys, torch; sys.path.insert(0, %r)\n"
+            "import fourier_basis_attention_b200 as fa\n"
+            "K = torch.zeros(1, 64, 8192, 128, dtype=torch.bfloat16, device='cuda')\n"
+            "src, dst = fa.PagedCache.dense(K, K), fa.PagedCache.dense(K[:, :, :16].clone(), K[:, :, :16].clone())\n"
+            "n = torch.tensor([8191], dtype=torch.int32, device='cuda')\n"
+            "b = fa.PagedBatch(src, 64, torch.tensor([0, 0], dtype=torch.int32, device='cuda'), n, 0, 0, 8191)\n"
+            "w = torch.arange(8192., device='cuda').repeat(1, 64, 1)\n"
+            "i = torch.zeros(1, 64, 16, dtype=torch.int32, device='cuda')\n"
+            "fa.fa_evict(b, w, 16, dst, i, torch.zeros_like(n))\n"
+            "fa.fa_device_status()\n"
+            "assert (i.cpu() == torch.arange(8175, 8191)).all()\n") % ROOT
+    subprocess.run([sys.executable, "-c", code], check=True, timeout=120)
 
 
 def test_evict_into_dense_then_compress():
