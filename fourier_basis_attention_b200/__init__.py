@@ -290,30 +290,55 @@ def _invalid(msg: str):
     raise FaError(FA_ERR_INVALID, msg)
 
 
-def _tensor(t, name: str, dtype, shape=None, rows: bool = False):
-    """Data pointer of a tensor on the current device. ``shape`` is compared where given
-    (None entries match anything); ``rows``: only the last two axes need to be dense."""
+def _device() -> int:
+    import torch
+    return torch.cuda.current_device()
+
+
+def _raw_stream(stream, device: int):
+    if stream is None:
+        import torch
+        return torch._C._cuda_getCurrentRawStream(device)
+    return getattr(stream, "cuda_stream", stream)
+
+
+def _why(t, name: str, dtype, shape, device: int, dense: int):
+    """Raise for a tensor that _tensor refused."""
     import torch
     if not isinstance(t, torch.Tensor):
         _invalid(f"{name} is not a tensor")
     if t.dtype != dtype:
         _invalid(f"{name} has dtype {t.dtype}, needs {dtype}")
-    if not t.is_cuda or t.get_device() != torch.cuda.current_device():
+    if t.dim() != len(shape) or any(n is not None and n != m for n, m in zip(shape, t.shape)):
+        _invalid(f"{name} has shape {tuple(t.shape)}, needs {tuple(shape)}")
+    if not t.is_cuda or t.get_device() != device:
         _invalid(f"{name} is on {t.device}, not on the current CUDA device")
-    if shape is not None and (t.dim() != len(shape) or any(
-            n is not None and n != m for n, m in zip(shape, t.shape))):
-        _invalid(f"{name} has shape {tuple(t.shape)}, needs {shape}")
-    if rows:
-        if t.numel() and (t.stride(-1) != 1 or (t.shape[-2] > 1 and t.stride(-2) != t.shape[-1])):
-            _invalid(f"{name}: the last two axes must be dense, strides are {t.stride()}")
-    elif not t.is_contiguous():
-        _invalid(f"{name} must be contiguous")
-    return t.data_ptr()
+    _invalid(f"{name}: the last {dense} axes must be dense, strides are {t.stride()}")
 
 
-def _token_stride(t) -> int:
-    """Elements between tokens of [tokens, heads, 128] (any value counts for a single token)."""
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * HEAD_DIM
+def _tensor(t, name: str, dtype, shape: tuple, device: int) -> int:
+    """Data pointer of a dense tensor of this type and shape on the current device."""
+    try:
+        if (t.dtype is dtype and t.shape == shape and t.get_device() == device
+                and t.is_contiguous()):
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    return _why(t, name, dtype, shape, device, len(shape))
+
+
+def _rows(t, name: str, shape: tuple, device: int):
+    """(pointer, elements between tokens) of a bf16 [tokens, heads, 128] tensor whose heads
+    are dense."""
+    import torch
+    try:
+        if t.dtype is torch.bfloat16 and t.shape == shape and t.get_device() == device:
+            st = t.stride()
+            if st[2] == 1 and (st[1] == HEAD_DIM or shape[1] == 1) or not t.numel():
+                return t.data_ptr(), st[0] if shape[0] > 1 else shape[1] * HEAD_DIM
+    except AttributeError:
+        pass
+    return _why(t, name, torch.bfloat16, shape, device, 2)
 
 
 class PagedCache:
@@ -323,9 +348,15 @@ class PagedCache:
 
     def __init__(self, K, V, page_table):
         import torch
-        self.pointers = (_tensor(K, "K", torch.bfloat16, (None, None, None, HEAD_DIM)),
-                         _tensor(V, "V", torch.bfloat16, tuple(K.shape)),
-                         _tensor(page_table, "page_table", torch.int32, (None, None)))
+        for t, name, dtype, dims in ((K, "K", torch.bfloat16, 4), (V, "V", torch.bfloat16, 4),
+                                     (page_table, "page_table", torch.int32, 2)):
+            if not isinstance(t, torch.Tensor) or t.dim() != dims:
+                _why(t, name, dtype, (None,) * dims, -1, dims)
+        device = _device() if K.is_cuda else -2
+        shape = (*K.shape[:3], HEAD_DIM)
+        self.pointers = (_tensor(K, "K", torch.bfloat16, shape, device),
+                         _tensor(V, "V", torch.bfloat16, shape, device),
+                         _tensor(page_table, "page_table", torch.int32, tuple(page_table.shape), device))
         self.K, self.V, self.page_table = K, V, page_table
         self.num_pages, self.Hkv, self.page_size = K.shape[:3]
         self.B, self.max_pages = page_table.shape
@@ -345,8 +376,9 @@ class PagedBatch:
     def __init__(self, cache: PagedCache, Hq: int, q_start, kv_len, total_q: int, max_q: int,
                  max_kv: int | None = None):
         import torch
-        starts = _tensor(q_start, "q_start", torch.int32, (cache.B + 1,))
-        lens = _tensor(kv_len, "kv_len", torch.int32, (cache.B,))
+        device = _device()
+        starts = _tensor(q_start, "q_start", torch.int32, (cache.B + 1,), device)
+        lens = _tensor(kv_len, "kv_len", torch.int32, (cache.B,), device)
         self.cache, self.q_start, self.kv_len = cache, q_start, kv_len
         self.Hq, self.total_q = Hq, total_q
         if max_kv is None:
@@ -356,6 +388,9 @@ class PagedBatch:
                                     cache.num_pages, cache.max_pages, total_q, max_q, max_kv)
         self.c = fa_paged_cache(*cache.pointers, starts, lens)
         self.refs = ctypes.byref(self.shape), ctypes.byref(self.c)
+        # shapes of q, of k and v, of lse
+        self.q_shape, self.kv_shape = (total_q, Hq, HEAD_DIM), (total_q, cache.Hkv, HEAD_DIM)
+        self.lse_shape = (total_q, Hq)
 
 
 def fa_rope_init(rot_dim: int = HEAD_DIM, base: float = 10000.0, interleaved: bool = False,
@@ -374,32 +409,33 @@ def fa_rope_init(rot_dim: int = HEAD_DIM, base: float = 10000.0, interleaved: bo
 _STRIDE3 = ctypes.c_int64 * 3
 
 
-def _row_ptr(t, name: str, dtype, shape):
-    """As _tensor, for tensors whose rows of 128 may lie anywhere."""
-    import torch
-    if t.dtype != dtype or t.shape != shape:
-        _invalid(f"{name} is {t.dtype} {tuple(t.shape)}, needs {dtype} {tuple(shape)}")
-    if not t.is_cuda or t.get_device() != torch.cuda.current_device():
-        _invalid(f"{name} is on {t.device}, not on the current CUDA device")
-    if t.numel() and t.stride(3) != 1:
-        _invalid(f"the last axis of {name} must be dense")
-    return t.data_ptr()
-
-
 def fa_rope(rope: fa_rope_plan, x, positions, out, transpose: bool = False, stream=None) -> None:
     """Rotate x (bf16 or fp32 [B, T, H, 128], any strides of the first three axes) at int32
     positions [B, T] into ``out``; ``transpose``: the transposed map, its gradient."""
     import torch
-    if x.dtype not in (torch.bfloat16, torch.float32):
-        _invalid(f"x has dtype {x.dtype}, needs bfloat16 or float32")
-    if x.dim() != 4 or x.shape[3] != HEAD_DIM:
-        _invalid(f"x has shape {tuple(x.shape)}, needs [B, T, H, 128]")
-    B, T, H, _ = x.shape
-    px, po = _row_ptr(x, "x", x.dtype, x.shape), _row_ptr(out, "out", x.dtype, x.shape)
-    pp = _tensor(positions, "positions", torch.int32, (B, T))
-    _check(LIB.fa_rope(rope, B, T, H, pp, px, _STRIDE3(*x.stride()[:3]), po,
-                       _STRIDE3(*out.stride()[:3]), FA_F32 if x.dtype == torch.float32 else FA_BF16,
-                       int(bool(transpose)), _stream(stream)))
+    dtype = FA_BF16
+    if x.dtype is not torch.bfloat16:
+        dtype = FA_F32
+        if x.dtype is not torch.float32:
+            _invalid(f"x has dtype {x.dtype}, needs bfloat16 or float32")
+    shape = x.shape
+    if len(shape) != 4 or shape[3] != HEAD_DIM:
+        _invalid(f"x has shape {tuple(shape)}, needs [B, T, H, 128]")
+    if not x.is_cuda:
+        _invalid(f"x is on {x.device}, not on the current CUDA device")
+    device = _device()
+    xs, ys = x.stride(), out.stride()
+    if x.get_device() != device:
+        _why(x, "x", x.dtype, shape, device, 1)
+    if out.dtype is not x.dtype or out.shape != shape or out.get_device() != device:
+        _why(out, "out", x.dtype, shape, device, 1)
+    if (xs[3] != 1 or ys[3] != 1) and x.numel():
+        _invalid(f"the last axis of x and out must be dense, strides are {xs} and {ys}")
+    B, T, H, _ = shape
+    pp = _tensor(positions, "positions", torch.int32, (B, T), device)
+    _check(LIB.fa_rope(rope, B, T, H, pp, x.data_ptr(), _STRIDE3(xs[0], xs[1], xs[2]), out.data_ptr(),
+                       _STRIDE3(ys[0], ys[1], ys[2]), dtype, 1 if transpose else 0,
+                       _raw_stream(stream, device)))
 
 
 def fa_paged_append(batch: PagedBatch, k, v, q=None, q_out=None, rope: fa_rope_plan | None = None,
@@ -407,31 +443,29 @@ def fa_paged_append(batch: PagedBatch, k, v, q=None, q_out=None, rope: fa_rope_p
     """Write the new tokens k, v (bf16 [total_q, Hkv, 128]) into the pages; with ``rope`` k, and
     q into q_out (bf16 [total_q, Hq, 128]), are rotated, at the cache index or ``positions``."""
     import torch
-    bf, n, c = torch.bfloat16, batch.total_q, batch.cache
-    qs = qos = 0
+    device = _device()
     pq = pqo = pp = None
+    qs = qos = 0
     if q is not None:
-        pq, qs = _tensor(q, "q", bf, (n, batch.Hq, HEAD_DIM), rows=True), _token_stride(q)
+        pq, qs = _rows(q, "q", batch.q_shape, device)
     if q_out is not None:
-        pqo = _tensor(q_out, "q_out", bf, (n, batch.Hq, HEAD_DIM), rows=True)
-        qos = _token_stride(q_out)
+        pqo, qos = _rows(q_out, "q_out", batch.q_shape, device)
     if positions is not None:
-        pp = _tensor(positions, "positions", torch.int32, (n,))
-    pk = _tensor(k, "k", bf, (n, c.Hkv, HEAD_DIM), rows=True)
-    pv = _tensor(v, "v", bf, (n, c.Hkv, HEAD_DIM), rows=True)
-    _check(LIB.fa_paged_append(*batch.refs, rope, pp, pq, qs, pqo, qos, pk, _token_stride(k), pv,
-                               _token_stride(v), _stream(stream)))
+        pp = _tensor(positions, "positions", torch.int32, (batch.total_q,), device)
+    pk, ks = _rows(k, "k", batch.kv_shape, device)
+    pv, vs = _rows(v, "v", batch.kv_shape, device)
+    _check(LIB.fa_paged_append(*batch.refs, rope, pp, pq, qs, pqo, qos, pk, ks, pv, vs,
+                               _raw_stream(stream, device)))
 
 
 def fa_paged_attend_workspace_size(batch: PagedBatch, window: int = 0) -> int:
     return LIB.fa_paged_attend_workspace_size(batch.refs[0], window)
 
 
-def _workspace(workspace):
-    import torch
+def _workspace(workspace, device: int):
     if workspace is None:
         return None, 0
-    if not workspace.is_cuda or workspace.get_device() != torch.cuda.current_device():
+    if workspace.get_device() != device:
         _invalid(f"workspace is on {workspace.device}, not on the current CUDA device")
     if not workspace.is_contiguous():
         _invalid("workspace must be contiguous")
@@ -443,13 +477,13 @@ def fa_paged_attend(batch: PagedBatch, q, out, workspace=None, lse=None, window:
     """Causal attention of the new tokens q (bf16 [total_q, Hq, 128], rotated) over the pages,
     their own keys included, into ``out`` (same shape); lse: fp32 [total_q, Hq] or None."""
     import torch
-    shape = (batch.total_q, batch.Hq, HEAD_DIM)
-    pq = _tensor(q, "q", torch.bfloat16, shape, rows=True)
-    po = _tensor(out, "out", torch.bfloat16, shape, rows=True)
-    pl = None if lse is None else _tensor(lse, "lse", torch.float32, shape[:2])
-    ws, size = _workspace(workspace)
-    _check(LIB.fa_paged_attend(*batch.refs, pq, _token_stride(q), scale, window, po,
-                               _token_stride(out), pl, ws, size, _stream(stream)))
+    device = _device()
+    pq, qs = _rows(q, "q", batch.q_shape, device)
+    po, os_ = _rows(out, "out", batch.q_shape, device)
+    pl = None if lse is None else _tensor(lse, "lse", torch.float32, batch.lse_shape, device)
+    ws, size = _workspace(workspace, device)
+    _check(LIB.fa_paged_attend(*batch.refs, pq, qs, scale, window, po, os_, pl, ws, size,
+                               _raw_stream(stream, device)))
 
 
 def fa_paged_weights(batch: PagedBatch, q, lse, weights, window: int = 0, scale: float = 0.0,
@@ -457,11 +491,19 @@ def fa_paged_weights(batch: PagedBatch, q, lse, weights, window: int = 0, scale:
     """Add to ``weights`` (fp32 [B, Hkv, >= max_kv]) what each key gets from the batch's
     queries; ``lse`` as fa_paged_attend wrote it for the same arguments."""
     import torch
-    pq = _tensor(q, "q", torch.bfloat16, (batch.total_q, batch.Hq, HEAD_DIM), rows=True)
-    pl = _tensor(lse, "lse", torch.float32, (batch.total_q, batch.Hq))
-    pw = _tensor(weights, "weights", torch.float32, (batch.cache.B, batch.cache.Hkv, None))
-    _check(LIB.fa_paged_weights(*batch.refs, pq, _token_stride(q), scale, window, pl, pw,
-                                weights.shape[2], _stream(stream)))
+    device = _device()
+    pq, qs = _rows(q, "q", batch.q_shape, device)
+    pl = _tensor(lse, "lse", torch.float32, batch.lse_shape, device)
+    pw, ld = _wide(weights, "weights", batch.cache, device)
+    _check(LIB.fa_paged_weights(*batch.refs, pq, qs, scale, window, pl, pw, ld,
+                                _raw_stream(stream, device)))
+
+
+def _wide(t, name: str, cache: PagedCache, device: int):
+    """(pointer, last size) of a dense fp32 [B, Hkv, any] tensor."""
+    import torch
+    last = t.shape[-1] if isinstance(t, torch.Tensor) and t.dim() == 3 else None
+    return _tensor(t, name, torch.float32, (cache.B, cache.Hkv, last), device), last
 
 
 def fa_evict_workspace_size(batch: PagedBatch, keep: int) -> int:
@@ -474,20 +516,17 @@ def fa_evict(batch: PagedBatch, weights, keep: int, dst: PagedCache, index, dst_
     ``recent``, then those of the largest ``weights``) and move them into the pages of ``dst``.
     index: int32 [B, Hkv, keep]; dst_len: int32 [B]; dst_weights: fp32 [B, Hkv, >= keep] or None."""
     import torch
-    c = batch.cache
-    pw = _tensor(weights, "weights", torch.float32, (c.B, c.Hkv, None))
-    pi = _tensor(index, "index", torch.int32, (c.B, c.Hkv, keep))
-    pn = _tensor(dst_len, "dst_len", torch.int32, (c.B,))
-    pd, ld = None, 0
-    if dst_weights is not None:
-        pd = _tensor(dst_weights, "dst_weights", torch.float32, (c.B, c.Hkv, None))
-        ld = dst_weights.shape[2]
-    ws, size = _workspace(workspace)
+    c, device = batch.cache, _device()
+    pw, wld = _wide(weights, "weights", c, device)
+    pi = _tensor(index, "index", torch.int32, (c.B, c.Hkv, keep), device)
+    pn = _tensor(dst_len, "dst_len", torch.int32, (c.B,), device)
+    pd, ld = (None, 0) if dst_weights is None else _wide(dst_weights, "dst_weights", c, device)
+    ws, size = _workspace(workspace, device)
     shape = fa_paged_shape(dst.B, dst.Hkv, dst.Hkv, HEAD_DIM, dst.page_size, dst.num_pages,
                            dst.max_pages, 0, 0, dst.max_pages * dst.page_size)
     cache = fa_paged_cache(*dst.pointers, None, None)
-    _check(LIB.fa_evict(*batch.refs, pw, weights.shape[2], keep, sink, recent, ctypes.byref(shape),
-                        ctypes.byref(cache), pd, ld, pi, pn, ws, size, _stream(stream)))
+    _check(LIB.fa_evict(*batch.refs, pw, wld, keep, sink, recent, ctypes.byref(shape),
+                        ctypes.byref(cache), pd, ld, pi, pn, ws, size, _raw_stream(stream, device)))
 
 
 def fa_device_status(stream=None) -> None:
