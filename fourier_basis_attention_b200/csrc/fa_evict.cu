@@ -67,6 +67,7 @@ __device__ __forceinline__ int4 ld_cluster_int4(uint32_t addr) {
 // One cluster of `size` CTAs a (sequence, KV head); CTA r has the tokens [r per, (r + 1) per).
 __global__ void __launch_bounds__(EV_THREADS)
     evict_select_kernel(const __grid_constant__ EvictParams P, int size, int held) {
+  allow_next_kernel();
   extern __shared__ __align__(16) uint32_t keys[];
   // counts of a digit, and their sums over the cluster; one histogram a digit, so that no CTA
   // waits for the others to have read it
@@ -239,6 +240,7 @@ __global__ void __launch_bounds__(EM_THREADS) evict_move_kernel(const __grid_con
   const int sub = threadIdx.x & 15;
   const long long bh = (long long)b * P.src.Hkv + g;
   int j[N];
+  wait_earlier_kernel();
 #pragma unroll
   for (int u = 0; u < N; ++u) {
     const int i = blockIdx.x * EM_ROWS + u * (EM_THREADS / 16) + (threadIdx.x >> 4);
@@ -326,8 +328,7 @@ cudaError_t launch_evict(const fa_paged_shape& s, const fa_paged_cache& c, const
   void* args[] = {&P, &size, &held};
   if ((e = cudaLaunchKernelExC(&cfg, fn, args)) != cudaSuccess) return e;
   const dim3 grid((unsigned)((keep + EM_ROWS - 1) / EM_ROWS), (unsigned)s.Hkv, (unsigned)s.B);
-  evict_move_kernel<<<grid, EM_THREADS, 0, stream>>>(P);
-  return cudaGetLastError();
+  return launch_overlapped(evict_move_kernel, grid, EM_THREADS, 0, stream, P);
 }
 
 }  // namespace fa

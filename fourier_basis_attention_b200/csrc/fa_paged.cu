@@ -156,6 +156,7 @@ __global__ void __launch_bounds__(PR_THREADS, 3)
                                              ~uintptr_t(1023));
   __shared__ uint64_t full[PR_WARPS][PR_STAGES];
   __shared__ int abort_word;
+  allow_next_kernel();
   const PagedBatch& p = P.p;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int slot = blockIdx.x % P.slots, tile = blockIdx.x / P.slots;
@@ -360,48 +361,68 @@ __global__ void __launch_bounds__(256) paged_join_kernel(const __grid_constant__
   const PagedBatch& p = P.p;
   const int lane = threadIdx.x & 31;
   const long long row = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
-  int b = 0, r, g;  // sequence, row of it in its KV head
+  int b = 0, r = 0, g = 0;  // sequence, row of it in its KV head
   SeqSpan s;
+  bool live = false;
   if (P.max_rows > 0) {
     r = (int)(row % P.max_rows);
     g = (int)(row / P.max_rows % p.Hkv);
     b = (int)(row / P.max_rows / p.Hkv);
-    if (b >= p.B) return;
-    s = seq_span(p, b);
-    if (r >= s.n * p.G || s.n * p.G > P.max_rows) return;
+    if (b < p.B) {
+      s = seq_span(p, b);
+      live = r < s.n * p.G && s.n * p.G <= P.max_rows;
+    }
   } else {
     const int t = (int)(row / p.Hq), h = (int)(row % p.Hq);
-    if (t >= p.total_q) return;
     for (int b0 = 0; b0 < p.B; b0 += 32) {
       const int i = b0 + lane + 1;
       const int n = __popc(__ballot_sync(0xFFFFFFFFu, i <= p.B && p.q_start[i] <= t));
       b += n;
       if (n < 32) break;
     }
-    if (b >= p.B) return;
-    s = seq_span(p, b);
-    if (t < s.q0 || t - s.q0 >= s.n || s.n * p.G <= P.min_rows) return;
-    g = h / p.G;
-    r = (t - s.q0) * p.G + h % p.G;
+    if (t < p.total_q && b < p.B) {
+      s = seq_span(p, b);
+      live = t >= s.q0 && t - s.q0 < s.n && s.n * p.G > P.min_rows;
+      g = h / p.G;
+      r = (t - s.q0) * p.G + h % p.G;
+    }
   }
+  wait_earlier_kernel();
+  if (!live) return;
   const int tile = r / P.tile_rows;
   int lo, hi;
   row_keys(s, p.G, P.window, tile * P.tile_rows, min((tile + 1) * P.tile_rows, s.n * p.G), &lo, &hi);
   const int slots = hi > lo ? (hi - 1) / P.chunk - lo / P.chunk + 1 : 1;
+  const float2* ml = P.part_ml + row * P.slots;
+  const float4* po = reinterpret_cast<const float4*>(P.part_o + row * P.slots * FA_HEAD_DIM) + lane;
   float mm = -INFINITY, ll = 0.0f;
   float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-  for (int k = 0; k < slots; ++k) {
-    const float2 e = P.part_ml[row * P.slots + k];
-    const float4 x = *reinterpret_cast<const float4*>(
-        P.part_o + (row * P.slots + k) * FA_HEAD_DIM + 4 * lane);
-    const float top = fmaxf(mm, e.x), base = top == -INFINITY ? 0.0f : top;
+  for (int k0 = 0; k0 < slots; k0 += 32) {  // lane k: chunk k0 + k
+    const float2 e = k0 + lane < slots ? ml[k0 + lane] : make_float2(-INFINITY, 0.0f);
+    float top = fmaxf(mm, e.x);
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
+    const float base = top == -INFINITY ? 0.0f : top;
     const float f = exp2_approx(mm - base), fe = exp2_approx(e.x - base);
     mm = top;
-    ll = ll * f + e.y * fe;
-    acc.x = acc.x * f + x.x * fe;
-    acc.y = acc.y * f + x.y * fe;
-    acc.z = acc.z * f + x.z * fe;
-    acc.w = acc.w * f + x.w * fe;
+    float l = e.y * fe;
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, d);
+    ll = ll * f + l;
+    acc.x *= f;
+    acc.y *= f;
+    acc.z *= f;
+    acc.w *= f;
+    const int n = min(32, slots - k0);
+#pragma unroll 8
+    for (int k = 0; k < n; ++k) {
+      const float4 x = po[(k0 + k) * (FA_HEAD_DIM / 4)];
+      const float w = __shfl_sync(0xFFFFFFFFu, fe, k);
+      acc.x = fmaf(w, x.x, acc.x);
+      acc.y = fmaf(w, x.y, acc.y);
+      acc.z = fmaf(w, x.z, acc.z);
+      acc.w = fmaf(w, x.w, acc.w);
+    }
   }
   const long long t = s.q0 + r / p.G;
   const int h = g * p.G + r % p.G;
@@ -421,6 +442,7 @@ __global__ void __launch_bounds__(PR_THREADS, 4)
                                              ~uintptr_t(1023));
   __shared__ uint64_t full[PR_WARPS][PW_STAGES];
   __shared__ int abort_word;
+  allow_next_kernel();
   const PagedBatch& p = P.p;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = blockIdx.y, b = blockIdx.z;
@@ -669,8 +691,7 @@ cudaError_t launch_paged_attend(const fa_paged_shape& s, const fa_paged_cache& c
     J.part_o = o;
     J.part_ml = ml;
     const long long rows = max_rows > 0 ? (long long)s.B * s.Hkv * max_rows : (long long)s.total_q * s.Hq;
-    paged_join_kernel<<<(unsigned)((rows + 7) / 8), 256, 0, stream>>>(J);
-    return cudaGetLastError();
+    return launch_overlapped(paged_join_kernel, dim3((unsigned)((rows + 7) / 8)), 256, 0, stream, J);
   };
   if (P.slots > 1 &&
       (e = join(P.chunk, P.slots, PR_ROWS, P.max_rows, 0, part_o, part_ml)) != cudaSuccess)

@@ -62,6 +62,32 @@ __device__ __forceinline__ void row_keys(const SeqSpan& s, int G, int window, in
   *lo = window > 0 ? max(0, first - window + 1) : 0;
 }
 
+// Overlap with the kernel launched next: it may be set up once every CTA of this one runs (or
+// has left), and waits for this one to complete where it calls wait_earlier_kernel. One that
+// needs none of its results calls it at its end, so that its completion covers both.
+__device__ __forceinline__ void allow_next_kernel() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+__device__ __forceinline__ void wait_earlier_kernel() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+// Launches a kernel that may be set up while the one before it on the stream still runs.
+template <typename... A, typename... B>
+cudaError_t launch_overlapped(void (*kernel)(A...), dim3 grid, int threads, size_t smem,
+                              cudaStream_t stream, const B&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3((unsigned)threads, 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 __device__ __forceinline__ float exp2_approx(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));

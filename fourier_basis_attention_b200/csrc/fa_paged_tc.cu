@@ -110,9 +110,8 @@ __device__ __forceinline__ void drain_ring(uint64_t* full, int issued) {
   }
 }
 
-__global__ void __launch_bounds__(PT_THREADS, 1)
-    paged_tile_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
-                      const __grid_constant__ CUtensorMap tv, const __grid_constant__ TileParams P) {
+__device__ __forceinline__ void attend_tiles(const CUtensorMap& tq, const CUtensorMap& tk,
+                                             const CUtensorMap& tv, const TileParams& P) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
@@ -420,6 +419,14 @@ __global__ void __launch_bounds__(PT_THREADS, 1)
   }
 }
 
+__global__ void __launch_bounds__(PT_THREADS, 1)
+    paged_tile_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
+                      const __grid_constant__ CUtensorMap tv, const __grid_constant__ TileParams P) {
+  allow_next_kernel();
+  attend_tiles(tq, tk, tv, P);
+  wait_earlier_kernel();  // the rows of short sequences: this kernel needs none of them
+}
+
 // Weights that keys gather: w_j += sum_rows exp2(c s_rj - log2 e lse_r). A CTA keeps 256 keys
 // (two tiles) and streams the query rows that see them in blocks of 128, as S^T = K Q^T: a
 // thread owns a key (a lane of tensor memory) and sums along its columns, so that nothing is
@@ -439,10 +446,8 @@ struct WeightParams {
   long long weights_ld;
 };
 
-__global__ void __launch_bounds__(PT_THREADS, 1)
-    paged_weights_tile_kernel(const __grid_constant__ CUtensorMap tq,
-                              const __grid_constant__ CUtensorMap tk,
-                              const __grid_constant__ WeightParams P) {
+__device__ __forceinline__ void sum_weight_tiles(const CUtensorMap& tq, const CUtensorMap& tk,
+                                                 const WeightParams& P) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
@@ -654,6 +659,15 @@ __global__ void __launch_bounds__(PT_THREADS, 1)
   }
 }
 
+__global__ void __launch_bounds__(PT_THREADS, 1)
+    paged_weights_tile_kernel(const __grid_constant__ CUtensorMap tq,
+                              const __grid_constant__ CUtensorMap tk,
+                              const __grid_constant__ WeightParams P) {
+  allow_next_kernel();
+  sum_weight_tiles(tq, tk, P);
+  wait_earlier_kernel();  // the keys of short sequences: this kernel needs none of them
+}
+
 FA_WATCHDOG_READER(read_watchdog_paged_tc)
 
 // ------------------------------------------------------------------------- host side
@@ -737,8 +751,7 @@ cudaError_t launch_tiles(const fa_paged_shape& s, const fa_paged_cache& c, const
   cudaError_t e = raise_smem_limit(fn, PT_SMEM);
   if (e != cudaSuccess) return e;
   const long long ctas = (long long)t.tiles * t.slots * s.Hkv;
-  paged_tile_kernel<<<(unsigned)ctas, PT_THREADS, PT_SMEM, stream>>>(tq, tk, tv, P);
-  return cudaGetLastError();
+  return launch_overlapped(paged_tile_kernel, dim3((unsigned)ctas), PT_THREADS, PT_SMEM, stream, tq, tk, tv, P);
 }
 
 cudaError_t launch_weight_tiles(const fa_paged_shape& s, const fa_paged_cache& c, const void* q,
@@ -766,8 +779,7 @@ cudaError_t launch_weight_tiles(const fa_paged_shape& s, const fa_paged_cache& c
   if (e != cudaSuccess) return e;
   const int max_q = s.max_q < s.total_q ? s.max_q : s.total_q;
   const dim3 grid((unsigned)chunk_slots(s, window, PV_KEYS, max_q), (unsigned)s.Hkv, (unsigned)s.B);
-  paged_weights_tile_kernel<<<grid, PT_THREADS, PV_SMEM, stream>>>(tq, tk, P);
-  return cudaGetLastError();
+  return launch_overlapped(paged_weights_tile_kernel, grid, PT_THREADS, PV_SMEM, stream, tq, tk, P);
 }
 
 }  // namespace fa
