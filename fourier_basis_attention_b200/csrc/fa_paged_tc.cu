@@ -15,6 +15,8 @@
 #include <math.h>
 #include <string.h>
 
+#include <type_traits>
+
 #include "fa_paged.cuh"
 
 namespace fa {
@@ -24,9 +26,19 @@ constexpr int PT_TILE = 128;                  // rows a tile
 constexpr int PT_HALF = 128 * 128;            // 64 dims x 128 rows
 constexpr int PT_BLOCK = 2 * PT_HALF;         // bytes of a block of K, V or Q rows
 constexpr int PT_STAGES = 5;
-constexpr int PT_WARPS = 12;                  // 4 + 4 softmax; producer, MMA and two idle ones
+constexpr int PT_SOFT = 8;                    // warps that turn scores into weights
+constexpr int PT_WARPS = PT_SOFT + 4;         // and producer, MMA, log-sum-exp and an idle one
 constexpr int PT_THREADS = PT_WARPS * 32;
-constexpr int PT_SMEM = (2 + PT_STAGES) * PT_BLOCK + 1024;
+
+// What the warps of the attention kernel share besides the blocks (no static arrays: the blocks
+// start at the aligned beginning of shared memory).
+struct TileShared {
+  uint64_t full[PT_STAGES], empty[PT_STAGES], q_full, s_full[2], p_full[4], o_full[2], drained;
+  uint32_t tmem;
+  int abort;
+};
+constexpr int PT_SMEM = (2 + PT_STAGES) * PT_BLOCK + (int)sizeof(TileShared);
+static_assert(PT_SMEM <= 232448, "fits the SM");
 constexpr float PT_SLACK = 8.0f;              // log2 by which the maximum may pass m
 
 struct TileParams {
@@ -42,6 +54,20 @@ struct TileParams {
   float2* part_ml;  // [row][slot]
 };
 
+// Waits for this thread's loads from tensor memory; the values depend on the wait, so that no
+// use of them moves before it.
+__device__ __forceinline__ void tmem_ld_wait_for(uint32_t (&a)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(a[0]), "+r"(a[1]), "+r"(a[2]), "+r"(a[3]), "+r"(a[4]), "+r"(a[5]), "+r"(a[6]), "+r"(a[7]),
+                 "+r"(a[8]), "+r"(a[9]), "+r"(a[10]), "+r"(a[11]), "+r"(a[12]), "+r"(a[13]), "+r"(a[14]), "+r"(a[15]),
+                 "+r"(a[16]), "+r"(a[17]), "+r"(a[18]), "+r"(a[19]), "+r"(a[20]), "+r"(a[21]), "+r"(a[22]),
+                 "+r"(a[23]), "+r"(a[24]), "+r"(a[25]), "+r"(a[26]), "+r"(a[27]), "+r"(a[28]), "+r"(a[29]),
+                 "+r"(a[30]), "+r"(a[31]));
+}
+__device__ __forceinline__ void tmem_ld_wait_for(uint32_t (&a)[32], uint32_t (&b)[32]) {
+  tmem_ld_wait_for(a);
+  tmem_ld_wait_for(b);
+}
 __device__ __forceinline__ uint64_t pack2(float a, float b) {
   uint64_t r;
   asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
@@ -61,6 +87,69 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   return r;
 }
 
+// The thread of a warp that issues the matrix instructions. They take their operands from
+// uniform registers: with a lane number as the condition every operand is moved there one by
+// one (100 clocks an instruction, measured, against the 64 that it runs).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(p));
+  return p != 0;
+}
+// Shared-memory descriptors in the 128-byte swizzle with 8-row groups 1024 bytes apart: the
+// high word is the same for all, the low one holds the address and the leading byte offset.
+constexpr uint32_t PT_DESC_HI = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t desc_lo(uint32_t addr, uint32_t lbo) {
+  return (addr >> 4) | ((lbo >> 4) << 16);
+}
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t idesc, bool add) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
+      "setp.ne.b32 p, %5, 0;\n\t"
+      "mov.b64 a, {%1, %3};\n\tmov.b64 b, {%2, %3};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, p;\n\t}" ::"r"(d),
+      "r"(a_lo), "r"(b_lo), "r"(PT_DESC_HI), "r"(idesc), "r"((uint32_t)add)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a_tmem, uint32_t b_lo, uint32_t idesc, bool add) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\t"
+      "setp.ne.b32 p, %5, 0;\n\t"
+      "mov.b64 b, {%2, %3};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n\t}" ::"r"(d),
+      "r"(a_tmem), "r"(b_lo), "r"(PT_DESC_HI), "r"(idesc), "r"((uint32_t)add)
+      : "memory");
+}
+
+// 2^y of a pair on the FMA units: y = n + f with n whole and f in [-1/2, 1/2] (adding and
+// subtracting 1.5 * 2^23 rounds), a polynomial for 2^f (the minimax one by the Remez exchange
+// for the relative error, 7.5e-8 at degree 5), n added to its exponent.
+// Arguments below -125 count as -125, minus infinity and NaN too.
+__device__ __forceinline__ void exp2_pair(uint64_t y, float* a, float* b) {
+  float y0, y1;
+  unpack2(y, &y0, &y1);
+  y = pack2(fmaxf(y0, -125.0f), fmaxf(y1, -125.0f));
+  const uint64_t magic = pack2(12582912.0f, 12582912.0f);
+  const uint64_t t = add2(y, magic);
+  const uint64_t f = add2(y, fma2(t, pack2(-1.0f, -1.0f), magic));
+  uint64_t p = fma2(f, pack2(1.327647245e-03f, 1.327647245e-03f), pack2(9.675540961e-03f, 9.675540961e-03f));
+  p = fma2(f, p, pack2(5.550713092e-02f, 5.550713092e-02f));
+  p = fma2(f, p, pack2(2.402212024e-01f, 2.402212024e-01f));
+  p = fma2(f, p, pack2(6.931469440e-01f, 6.931469440e-01f));
+  p = fma2(f, p, pack2(1.000000119e+00f, 1.000000119e+00f));
+  float p0, p1, t0, t1;
+  unpack2(p, &p0, &p1);
+  unpack2(t, &t0, &t1);
+  *a = __int_as_float(__float_as_int(p0) + (__float_as_int(t0) << 23));
+  *b = __int_as_float(__float_as_int(p1) + (__float_as_int(t1) << 23));
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
 // Issues the boxes of 128 keys [j0, j0 + 128) of a pool: lanes 0 .. 2 * (128 / box) - 1 hold
 // one box each; `row` is the lane's row in the pool (key_row).
 __device__ __forceinline__ void load_keys(uint8_t* dst, const CUtensorMap* map, uint64_t* bar, int box,
@@ -70,6 +159,18 @@ __device__ __forceinline__ void load_keys(uint8_t* dst, const CUtensorMap* map, 
     const int half = lane >= n, i = lane - half * n;
     tma_load_2d(dst + half * PT_HALF + i * box * 128, map, bar, 64 * half, row);
   }
+}
+
+// Zeroes rows [0, lo) and [hi, 128) of a block: two rows a turn, 16 lanes each.
+__device__ __forceinline__ void hide_values(uint8_t* block, int lo, int hi, int lane) {
+  uint8_t* at = block + ((lane >> 3) & 1) * PT_HALF + (lane >> 4) * 128 + (lane & 7) * 16;
+  const int up = max(hi, 0) + (lane >> 4);
+#pragma unroll 4
+  for (int r = lane >> 4; r < lo; r += 2)
+    *reinterpret_cast<uint4*>(at + (r & ~1) * 128) = make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll 4
+  for (int r = up; r < PT_KEYS; r += 2)
+    *reinterpret_cast<uint4*>(at + (r - (lane >> 4)) * 128) = make_uint4(0u, 0u, 0u, 0u);
 }
 
 // Row of the pools at which this lane's box of block j0 starts. Boxes without a key of
@@ -83,6 +184,13 @@ __device__ __forceinline__ int key_row(const PagedBatch& p, int b, int g, int j0
   if (j >= hi || j + box <= lo) return none;
   const int pg = page_of(p, b, j);
   return pg < 0 ? none : (pg * p.Hkv + g) * p.page + j % p.page;
+}
+
+// Blocks [a, e), counted from key k_lo, of the CTA's nb that tokens [first, first + n) see.
+__device__ __forceinline__ void tile_blocks(int first, int n, int window, int k_lo, int nb, int* a, int* e) {
+  const int lo = window > 0 ? max(0, first - window + 1) : 0, hi = n > 0 ? max(0, first + n) : 0;
+  *a = max(0, lo / PT_KEYS - k_lo / PT_KEYS);
+  *e = max(*a, min(nb, (hi + PT_KEYS - 1) / PT_KEYS - k_lo / PT_KEYS));
 }
 
 // The sequence of tile x: tiles of T tokens, those of sequence b from q_start[b] / T + b on
@@ -112,13 +220,14 @@ __device__ __forceinline__ void drain_ring(uint64_t* full, int issued) {
 
 __device__ __forceinline__ void attend_tiles(const CUtensorMap& tq, const CUtensorMap& tk,
                                              const CUtensorMap& tv, const TileParams& P) {
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
-                                             ~uintptr_t(1023));
+  extern __shared__ __align__(1024) uint8_t smem[];
   uint8_t* ring = smem + 2 * PT_BLOCK;
-  __shared__ uint64_t full[PT_STAGES], empty[PT_STAGES], q_full, s_full[2], p_full[2], drained;
-  __shared__ uint32_t tmem_ptr;
-  __shared__ int abort_word;
+  TileShared& sh = *reinterpret_cast<TileShared*>(ring + PT_STAGES * PT_BLOCK);
+  uint64_t *full = sh.full, *empty = sh.empty, *s_full = sh.s_full, *p_full = sh.p_full;
+  if (smem_u32(smem) & 1023u) {  // the swizzle counts from 1024-byte boundaries
+    flag_entry(WD_PAGED | 19u);
+    return;
+  }
   const PagedBatch& p = P.p;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = blockIdx.x % p.Hkv, rest = blockIdx.x / p.Hkv;
@@ -138,47 +247,53 @@ __device__ __forceinline__ void attend_tiles(const CUtensorMap& tq, const CUtens
   const int k_lo = max(lo & ~(PT_KEYS - 1), c0), k_hi = min(hi, c0 + P.chunk);
   const int nb = k_hi > k_lo ? (k_hi - k_lo + PT_KEYS - 1) / PT_KEYS : 0;
   if (nb == 0 && !(single || (slot == 0 && hi <= lo))) return;  // the merge skips it
+  int a0, a1, e0, e1;  // blocks that tiles 0 and 1 see
+  tile_blocks(p0, min(P.tok, n_tok), P.window, k_lo, nb, &a0, &e0);
+  tile_blocks(p0 + P.tok, n_tok - P.tok, P.window, k_lo, nb, &a1, &e1);
 
   if (threadIdx.x == 0) {
-    abort_word = 0;
+    sh.abort = 0;
     for (int i = 0; i < PT_STAGES; ++i) {
       mbar_init(&full[i], 1);
       mbar_init(&empty[i], 1);
     }
-    mbar_init(&q_full, 1);
-    mbar_init(&drained, 1);
+    mbar_init(&sh.q_full, 1);
+    mbar_init(&sh.drained, 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s_full[i], 1);
-      mbar_init(&p_full[i], 4);
+      mbar_init(&sh.o_full[i], 1);
     }
+    for (int i = 0; i < 4; ++i) mbar_init(&p_full[i], 4);
     fence_barrier_init();
   }
-  if (warp == 9) {
-    tmem_alloc(&tmem_ptr, 512);
+  if (warp == PT_SOFT + 1) {
+    tmem_alloc(&sh.tmem, 512);
     tmem_relinquish();
     tc_fence_before();
   }
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = tmem_ptr;  // S / P of tiles 0, 1 at columns 0, 128; O at 256, 384
-  volatile int* abort_flag = &abort_word;
+  const uint32_t tmem = sh.tmem;  // S / P of tiles 0, 1 at columns 0, 128; O at 256, 384
+  volatile int* abort_flag = &sh.abort;
   // 168 registers a thread at launch: 8 warps take 208, 4 keep 88 (the sum is the same)
-  if (warp >= 8) {
+  if (warp >= PT_SOFT) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
-  if (warp == 8) {
+  if (warp == PT_SOFT) {
     // ------------------------------------------------------------------ producer
     int issued = 0;
     if (nb > 0) {
       const int q_bytes = P.tok * p.G * 128;  // of one 64-dim half of a tile
       if (lane == 0) {
-        mbar_arrive_expect_tx(&q_full, (uint32_t)(q_bytes * (two ? 4 : 2)));
+        mbar_arrive_expect_tx(&sh.q_full, (uint32_t)(q_bytes * (two ? 4 : 2)));
         for (int i = 0; i < (two ? 4 : 2); ++i)
-          tma_load_3d(smem + (i >> 1) * PT_BLOCK + (i & 1) * PT_HALF, &tq, &q_full, 64 * (i & 1),
+          tma_load_3d(smem + (i >> 1) * PT_BLOCK + (i & 1) * PT_HALF, &tq, &sh.q_full, 64 * (i & 1),
                       g * p.G, s.q0 + t0 + (i >> 1) * P.tok);
       }
       bool ok = true;
+      int next = key_row(p, b, g, k_lo, P.box, lo, hi, lane);
       for (int i = 0; i < nb && ok; ++i) {
-        const int row = key_row(p, b, g, k_lo + i * PT_KEYS, P.box, lo, hi, lane);
+        const int row = next;  // looked up a block ahead: the page table answers in 0.5 us
+        if (i + 1 < nb) next = key_row(p, b, g, k_lo + (i + 1) * PT_KEYS, P.box, lo, hi, lane);
 #pragma unroll
         for (int v = 0; v < 2; ++v) {
           const int st = issued % PT_STAGES;
@@ -194,87 +309,88 @@ __device__ __forceinline__ void attend_tiles(const CUtensorMap& tq, const CUtens
       }
       if (!ok && lane == 0) {
         drain_ring<PT_STAGES>(full, issued);
-        drain_ring<1>(&q_full, 1);
+        drain_ring<1>(&sh.q_full, 1);
       }
     }
-  } else if (warp == 9) {
-    // ------------------------------------------------------------------ MMA
+  } else if (warp == PT_SOFT + 1) {
+    // ------------------------------------------------------------------ MMA: one warp for both
+    // tiles, so that their products run one after the other and not interleaved
     constexpr uint32_t id_s = idesc_bf16_f32(PT_TILE, PT_KEYS, false);
     constexpr uint32_t id_o = idesc_bf16_f32(PT_TILE, FA_HEAD_DIM, true);
-    const uint32_t q_addr = smem_u32(smem), r_addr = smem_u32(ring);
+    const uint32_t q_lo = desc_lo(smem_u32(smem), 16), kb_lo = desc_lo(smem_u32(ring), 16);
+    const uint32_t v_lo = desc_lo(smem_u32(ring), PT_HALF);
     auto scores = [&](int t, int st) {
+      const uint32_t qa = q_lo + t * (PT_BLOCK >> 4), kb = kb_lo + st * (PT_BLOCK >> 4);
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
-        const uint32_t off = (k >> 2) * PT_HALF + (k & 3) * 32;
-        mma_f16(tmem + 128 * t, smem_desc_sw128(q_addr + t * PT_BLOCK + off, 16, 1024),
-                smem_desc_sw128(r_addr + st * PT_BLOCK + off, 16, 1024), id_s, k > 0 ? 1u : 0u);
+        const uint32_t off = ((k >> 2) * PT_HALF + (k & 3) * 32) >> 4;
+        mma_ss(tmem + 128 * t, qa + off, kb + off, id_s, k > 0);
       }
       mma_commit(&s_full[t]);
     };
-    bool ok = nb > 0 && mbar_wait(&q_full, 0, abort_flag, WD_PAGED | 4u);
-    int c = 0;  // ring use
-    auto use = [&]() {
-      const int st = c % PT_STAGES;
-      ok = ok && mbar_wait(&full[st], (uint32_t)(c / PT_STAGES) & 1u, abort_flag, WD_PAGED | 5u);
-      ok = __all_sync(0xFFFFFFFFu, ok);
-      tc_fence_after();
-      ++c;
-      return st;
+    auto loaded = [&](int c) {  // use c of the ring
+      return mbar_wait(&full[c % PT_STAGES], (uint32_t)(c / PT_STAGES) & 1u, abort_flag, WD_PAGED | 5u);
     };
-    if (nb > 0) {
-      const int st = use();
-      if (ok && lane == 0) {
-        scores(0, st);
-        if (two) scores(1, st);
-        mma_commit(&empty[st]);
-      }
+    bool ok = nb > 0 && mbar_wait(&sh.q_full, 0, abort_flag, WD_PAGED | 4u) && loaded(0);
+    if (__all_sync(0xFFFFFFFFu, ok) && elect_one()) {
+      if (a0 == 0 && e0 > 0) scores(0, 0);
+      if (a1 == 0 && e1 > 0) scores(1, 0);
+      mma_commit(&empty[0]);
     }
-    for (int i = 0; i < nb && ok; ++i) {
-      const int sv = use();
+    for (int i = 0; i < nb; ++i) {
+      const int sv = (2 * i + 1) % PT_STAGES, sk = (2 * i + 2) % PT_STAGES;
+      const bool more = i + 1 < nb;
+      // a wait that finds its phase complete still takes some 100 clocks: these come while the
+      // tensor core has work
+      ok = ok && loaded(2 * i + 1) && (!more || loaded(2 * i + 2));
       const int j0 = k_lo + i * PT_KEYS;
       if (ok && (j0 < lo || j0 + PT_KEYS > hi)) {
         // values of keys outside [lo, hi) may be anything, NaN too: they count as zero
-        uint8_t* v = ring + sv * PT_BLOCK;
-        for (int w = lane; w < PT_KEYS * 16; w += 32) {
-          const int r = w >> 4;
-          if (j0 + r < lo || j0 + r >= hi)
-            *reinterpret_cast<uint4*>(v + ((w >> 3) & 1) * PT_HALF + r * 128 + (w & 7) * 16) =
-                make_uint4(0u, 0u, 0u, 0u);
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
+        hide_values(ring + sv * PT_BLOCK, lo - j0, hi - j0, lane);
+            fence_proxy_async_smem();
       }
-      int sk = -1;
-      for (int t = 0; t < 1 + two && ok; ++t) {
-        ok = mbar_wait(&p_full[t], (uint32_t)i & 1u, abort_flag, WD_PAGED | 6u);
-        ok = __all_sync(0xFFFFFFFFu, ok);
-        if (!ok) break;
-        tc_fence_after();
-        if (lane == 0) {
+      for (int t = 0; t < 2 && ok; ++t) {
+        const int a = t ? a1 : a0, e = t ? e1 : e0;
+        if (a <= i && i < e) {
+          // the weights of keys 0-63 and 64-127 of the block: the first product runs while the
+          // others are still computed
 #pragma unroll
-          for (int k = 0; k < 8; ++k)
-            mma_f16_ta(tmem + 256 + 128 * t, tmem + 128 * t + 8 * k,
-                       smem_desc_sw128(r_addr + sv * PT_BLOCK + 2048 * k, PT_HALF, 1024), id_o,
-                       i > 0 || k > 0 ? 1u : 0u);
-          if (t == two) mma_commit(&empty[sv]);
-        }
-        if (i + 1 < nb) {
-          if (t == 0) sk = use();
-          if (!ok) break;
-          if (lane == 0) {
-            scores(t, sk);
-            if (t == two) mma_commit(&empty[sk]);
+          for (int h = 0; h < 2; ++h) {
+            ok = ok && mbar_wait(&p_full[2 * t + h], (uint32_t)(i - a) & 1u, abort_flag, WD_PAGED | 6u);
+            if (!__all_sync(0xFFFFFFFFu, ok)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            if (elect_one()) {
+#pragma unroll
+              for (int k = 4 * h; k < 4 * h + 4; ++k)
+                mma_ts(tmem + 256 + 128 * t, tmem + 128 * t + 8 * k, v_lo + (sv * PT_BLOCK + 2048 * k) / 16,
+                       id_o, i > a || k > 0);
+              if (h == 1) {
+                if (more && i + 1 < e) scores(t, sk);
+                if (i + 1 == e) mma_commit(&sh.o_full[t]);
+              }
+            }
           }
-        } else if (lane == 0) {
-          mma_commit(&s_full[t]);  // O is complete
+        } else if (more && i + 1 == a && a < e) {
+          if (elect_one()) scores(t, sk);
         }
+      }
+      if (!__all_sync(0xFFFFFFFFu, ok)) {
+        ok = false;
+        break;
+      }
+      if (elect_one()) {
+        mma_commit(&empty[sv]);
+        if (more) mma_commit(&empty[sk]);
       }
     }
-    if (nb > 0 && !ok && lane == 0) {
+    if (nb > 0 && !ok && elect_one()) {
       // tensor memory is released only after every MMA of this CTA has completed
-      mma_commit(&drained);
+      mma_commit(&sh.drained);
       const unsigned long long w0 = globaltimer_ns();
-      while (!mbar_try_wait(&drained, 0))
+      while (!mbar_try_wait(&sh.drained, 0))
         if (globaltimer_ns() - w0 > 200000000ull) break;
     }
   }
@@ -284,41 +400,47 @@ __device__ __forceinline__ void attend_tiles(const CUtensorMap& tq, const CUtens
     // ------------------------------------------------------------------ softmax, one row a thread
     const int t = warp >> 2, row = threadIdx.x & 127;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-    const uint32_t ts = tmem + 128 * t + lanes, to = tmem + 256 + 128 * t + lanes;
+    const uint32_t ts = tmem + 128 * t + lanes, to = ts + 256;
     const int tok = t * P.tok + row / p.G;
     const bool valid = row < P.tok * p.G && tok < n_tok;
     const int pos = valid ? p0 + tok : -1;
-    const int p_first = p0 + t * P.tok, p_last = min(p_first + P.tok, p0 + n_tok) - 1;
+    // positions of the warp's rows, blocks of the tile
+    const int pw_first = p0 + t * P.tok + (row & ~31) / p.G;
+    const int pw_last = p0 + min(t * P.tok + min((row | 31) / p.G, P.tok - 1), n_tok - 1);
+    const int a = t ? a1 : a0, e_ = t ? e1 : e0;
     const float c = P.scale_log2;
     float m = -INFINITY, l = 0.0f;
     bool ok = true;
-    for (int i = 0; i < nb; ++i) {
-      ok = mbar_wait(&s_full[t], (uint32_t)i & 1u, abort_flag, WD_PAGED | 7u);
+    for (int i = a; i < e_; ++i) {
+      ok = mbar_wait(&s_full[t], (uint32_t)(i - a) & 1u, abort_flag, WD_PAGED | 7u);
       ok = __all_sync(0xFFFFFFFFu, ok);
       if (!ok) break;
       tc_fence_after();
       uint32_t sr[4][32];
-#pragma unroll
-      for (int v = 0; v < 4; ++v) tmem_ld_32x32b_x32(ts + 32 * v, sr[v]);
-      tmem_ld_wait();
       const int j0 = k_lo + i * PT_KEYS;
-      if (j0 + PT_KEYS > p_first + 1 || (P.window > 0 && j0 <= p_last - P.window)) {
-        const int up = pos - j0, down = P.window > 0 ? pos - P.window - j0 : -1;
-#pragma unroll
-        for (int v = 0; v < 4; ++v)
-#pragma unroll
-          for (int e = 0; e < 32; ++e)
-            if (32 * v + e > up || 32 * v + e <= down) sr[v][e] = 0xFF800000u;
-      }
-      float mx[4];
+      tmem_ld_32x32b_x32(ts, sr[0]);
+      tmem_ld_32x32b_x32(ts + 32, sr[1]);
+      tmem_ld_wait_for(sr[0], sr[1]);
+      tmem_ld_32x32b_x32(ts + 64, sr[2]);
+      tmem_ld_32x32b_x32(ts + 96, sr[3]);
+      float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
       for (int v = 0; v < 4; ++v) {
-        mx[v] = __uint_as_float(sr[v][0]);
+        if (v == 2) tmem_ld_wait_for(sr[2], sr[3]);
+        // chunks of 32 keys that some row of the warp does not see
+        const int j = j0 + 32 * v;
+        if (j + 31 > pw_first || (P.window > 0 && j <= pw_last - P.window)) {
+          const int up = pos - j, down = P.window > 0 ? up - P.window : -1;
 #pragma unroll
-        for (int e = 1; e < 32; ++e) mx[v] = fmaxf(mx[v], __uint_as_float(sr[v][e]));
+          for (int e = 0; e < 32; ++e)
+            if (e > up || e <= down) sr[v][e] = 0xFF800000u;
+        }
+#pragma unroll
+        for (int e = 0; e < 32; e += 2)
+          mx[(e >> 1) & 3] = max3(mx[(e >> 1) & 3], __uint_as_float(sr[v][e]), __uint_as_float(sr[v][e + 1]));
       }
-      const float top = c * fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-      if (i == 0) {
+      const float top = c * max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]);
+      if (i == a) {
         m = top;
       } else {
         const bool behind = valid && top > m + PT_SLACK;
@@ -356,17 +478,17 @@ __device__ __forceinline__ void attend_tiles(const CUtensorMap& tq, const CUtens
           w[e] = pack_bf16(y0, y1);
         }
         tmem_st_32x32b_x32(ts + 32 * h, w);
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_full[2 * t + h]);
       }
-      tmem_st_wait();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&p_full[t]);
-      float a0, a1;
-      unpack2(add2(sum[0], sum[1]), &a0, &a1);
-      l += a0 + a1;
+      float l0, l1;
+      unpack2(add2(sum[0], sum[1]), &l0, &l1);
+      l += l0 + l1;
     }
-    if (nb > 0 && ok) {
-      ok = mbar_wait(&s_full[t], (uint32_t)nb & 1u, abort_flag, WD_PAGED | 8u);
+    if (e_ > a && ok) {
+      ok = mbar_wait(&sh.o_full[t], 0, abort_flag, WD_PAGED | 8u);
       ok = __all_sync(0xFFFFFFFFu, ok);
       tc_fence_after();
     }
@@ -378,7 +500,7 @@ __device__ __forceinline__ void attend_tiles(const CUtensorMap& tq, const CUtens
 #pragma unroll 1
       for (int v = 0; v < 4; ++v) {
         uint32_t o[32];
-        if (nb > 0) {
+        if (e_ > a) {
           tmem_ld_32x32b_x32(to + 32 * v, o);
           tmem_ld_wait();
         } else {
@@ -386,8 +508,9 @@ __device__ __forceinline__ void attend_tiles(const CUtensorMap& tq, const CUtens
           for (int e = 0; e < 32; ++e) o[e] = 0u;
         }
         if (!valid) continue;
+        const int d = 32 * v;
         if (single) {
-          uint4* dst = reinterpret_cast<uint4*>(P.out + token * P.out_stride + h * FA_HEAD_DIM + 32 * v);
+          uint4* dst = reinterpret_cast<uint4*>(P.out + token * P.out_stride + h * FA_HEAD_DIM + d);
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             uint32_t w[4];
@@ -398,7 +521,7 @@ __device__ __forceinline__ void attend_tiles(const CUtensorMap& tq, const CUtens
             dst[e] = make_uint4(w[0], w[1], w[2], w[3]);
           }
         } else {
-          uint4* dst = reinterpret_cast<uint4*>(P.part_o + rec * FA_HEAD_DIM + 32 * v);
+          uint4* dst = reinterpret_cast<uint4*>(P.part_o + rec * FA_HEAD_DIM + d);
 #pragma unroll
           for (int e = 0; e < 8; ++e)
             dst[e] = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
@@ -413,7 +536,7 @@ __device__ __forceinline__ void attend_tiles(const CUtensorMap& tq, const CUtens
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 9) {
+  if (warp == PT_SOFT + 1) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
@@ -433,6 +556,8 @@ __global__ void __launch_bounds__(PT_THREADS, 1)
 // reduced across threads and a key's sum is taken in one order. Scores are double-buffered:
 // the tensor core writes one buffer while the other is summed. Bound: 2 * 128 flops a (row,
 // key) against one exp2: 512 and 1024 clocks for a 128 x 128 tile.
+constexpr int PV_SOFT = 16;                   // warps that sum; 4 more as above
+constexpr int PV_THREADS = (PV_SOFT + 4) * 32;
 constexpr int PV_STAGES = 4;
 constexpr int PV_KEYS = 2 * PT_TILE;
 constexpr int PV_SMEM = (2 + PV_STAGES) * PT_BLOCK + 1024;
@@ -454,6 +579,7 @@ __device__ __forceinline__ void sum_weight_tiles(const CUtensorMap& tq, const CU
   uint8_t* ring = smem + 2 * PT_BLOCK;
   __shared__ uint64_t full[PV_STAGES], empty[PV_STAGES], k_full, s_full[4], s_empty[4], drained;
   __shared__ __align__(16) float minus_lse[PV_STAGES][PT_TILE];
+  __shared__ float half_sum[PV_KEYS];
   __shared__ uint32_t tmem_ptr;
   __shared__ int abort_word;
   const PagedBatch& p = P.p;
@@ -476,23 +602,23 @@ __device__ __forceinline__ void sum_weight_tiles(const CUtensorMap& tq, const CU
     abort_word = 0;
     for (int i = 0; i < PV_STAGES; ++i) {
       mbar_init(&full[i], 2);
-      mbar_init(&empty[i], 1 + 4 * (1 + two));
+      mbar_init(&empty[i], 1 + 8 * (1 + two));
     }
     mbar_init(&k_full, 1);
     mbar_init(&drained, 1);
     for (int i = 0; i < 4; ++i) {
       mbar_init(&s_full[i], 1);
-      mbar_init(&s_empty[i], 4);
+      mbar_init(&s_empty[i], 8);
     }
     fence_barrier_init();
   }
-  if (warp == 9) {
+  if (warp == PV_SOFT + 1) {
     tmem_alloc(&tmem_ptr, 512);
     tmem_relinquish();
     tc_fence_before();
   }
   // rows of the blocks that no box fills (128 is not a multiple of G) are zero
-  for (int w = threadIdx.x; w < PV_STAGES * 2 * (PT_TILE - P.tok * p.G) * 8; w += PT_THREADS) {
+  for (int w = threadIdx.x; w < PV_STAGES * 2 * (PT_TILE - P.tok * p.G) * 8; w += PV_THREADS) {
     const int pad = PT_TILE - P.tok * p.G, r = PT_TILE - 1 - w / 8 % pad, h = w / 8 / pad;
     *reinterpret_cast<uint4*>(ring + h * PT_HALF + r * 128 + (w & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
   }
@@ -502,9 +628,9 @@ __device__ __forceinline__ void sum_weight_tiles(const CUtensorMap& tq, const CU
   const uint32_t tmem = tmem_ptr;  // scores of tile t, buffer u at columns 128 (2 t + u)
   volatile int* abort_flag = &abort_word;
 
-  if (warp >= 8) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
-    if (warp == 8) {
+  if (warp >= PV_SOFT) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+    if (warp == PV_SOFT) {
       // ---------------------------------------------------------------- producer
       bool ok = true;
       int issued = 0;
@@ -532,10 +658,10 @@ __device__ __forceinline__ void sum_weight_tiles(const CUtensorMap& tq, const CU
         drain_ring<PV_STAGES>(full, issued);
         drain_ring<1>(&k_full, 1);
       }
-    } else if (warp == 9) {
+    } else if (warp == PV_SOFT + 1) {
       // ---------------------------------------------------------------- MMA
       constexpr uint32_t id = idesc_bf16_f32(PT_TILE, PT_TILE, false);
-      const uint32_t k_addr = smem_u32(smem), r_addr = smem_u32(ring);
+      const uint32_t a_lo = desc_lo(smem_u32(smem), 16), b_lo = desc_lo(smem_u32(ring), 16);
       bool ok = mbar_wait(&k_full, 0, abort_flag, WD_PAGED | 10u);
       for (int i = 0; i < nb; ++i) {
         const int st = i % PV_STAGES, u = i & 1;
@@ -546,69 +672,76 @@ __device__ __forceinline__ void sum_weight_tiles(const CUtensorMap& tq, const CU
           ok = __all_sync(0xFFFFFFFFu, ok);
           if (!ok) break;
           tc_fence_after();
-          if (lane == 0) {
+          if (elect_one()) {
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
-              const uint32_t off = (k >> 2) * PT_HALF + (k & 3) * 32;
-              mma_f16(tmem + 128 * (2 * t + u), smem_desc_sw128(k_addr + t * PT_BLOCK + off, 16, 1024),
-                      smem_desc_sw128(r_addr + st * PT_BLOCK + off, 16, 1024), id, k > 0 ? 1u : 0u);
+              const uint32_t off = ((k >> 2) * PT_HALF + (k & 3) * 32) >> 4;
+              mma_ss(tmem + 128 * (2 * t + u), a_lo + t * (PT_BLOCK >> 4) + off,
+                     b_lo + st * (PT_BLOCK >> 4) + off, id, k > 0);
             }
             mma_commit(&s_full[2 * t + u]);
             if (t == two) mma_commit(&empty[st]);
           }
         }
+        __syncwarp();
         if (!ok) break;
       }
-      if (!ok && lane == 0) {
+      if (!ok && elect_one()) {
         mma_commit(&drained);
         const unsigned long long w0 = globaltimer_ns();
         while (!mbar_try_wait(&drained, 0))
           if (globaltimer_ns() - w0 > 200000000ull) break;
       }
-    } else if (warp == 10) {
-      // ---------------------------------------------------------------- log-sum-exp of the rows
-      for (int i = 0; i < nb; ++i) {
-        const int st = i % PV_STAGES;
-        float4 v;
-        float* e = &v.x;
+    } else if (warp == PV_SOFT + 2) {
+      // ---------------------------------------------------------------- log-sum-exp of the rows,
+      // loaded a block ahead
+      auto load = [&](int i, float (&e)[4]) {
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
           const int col = 4 * lane + x, tok = (blk0 + i) * P.tok + col / p.G;
-          e[x] = -INFINITY;  // columns without a row, and rows that see no key, add nothing
-          if (col < P.tok * p.G && tok < s.n) {
-            const float l = P.lse[(long long)(s.q0 + tok) * p.Hq + g * p.G + col % p.G];
-            if (l != -INFINITY) e[x] = -1.44269504088896341f * l;
-          }
+          e[x] = INFINITY;  // columns without a row add nothing
+          if (i < nb && col < P.tok * p.G && tok < s.n)
+            e[x] = P.lse[(long long)(s.q0 + tok) * p.Hq + g * p.G + col % p.G];
         }
+      };
+      float next[4];
+      load(0, next);
+      for (int i = 0; i < nb; ++i) {
+        const int st = i % PV_STAGES;
+        float e[4];
+#pragma unroll
+        for (int x = 0; x < 4; ++x)  // nor do rows that see no key
+          e[x] = next[x] == -INFINITY ? -INFINITY : -1.44269504088896341f * next[x];
+        load(i + 1, next);
         bool ok = true;
         if (i >= PV_STAGES)
           ok = mbar_wait(&empty[st], (uint32_t)(i / PV_STAGES - 1) & 1u, abort_flag, WD_PAGED | 13u);
         if (!__all_sync(0xFFFFFFFFu, ok)) break;
-        *reinterpret_cast<float4*>(&minus_lse[st][4 * lane]) = v;
+        *reinterpret_cast<float4*>(&minus_lse[st][4 * lane]) = make_float4(e[0], e[1], e[2], e[3]);
         __syncwarp();
         if (lane == 0) mbar_arrive(&full[st]);
       }
     }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
-    if ((warp >> 2) <= two) {
-      // ---------------------------------------------------------------- sums, one key a thread
-      const int t = warp >> 2;
-      const int j = j0 + threadIdx.x, jt = j0 + t * PT_TILE;
-      const uint32_t ts = tmem + 256 * t + ((uint32_t)((warp & 3) * 32) << 16);
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
+    // ------------------------------------------------------------------ sums: two threads a key,
+    // each with 64 columns of a block
+    const int t = warp >> 3, half = (warp >> 2) & 1, row = 32 * (warp & 3) + lane;
+    const int jt = j0 + t * PT_TILE, j = jt + row;
+    float total = 0.0f;
+    if (t <= two) {
+      const uint32_t ts = tmem + 256 * t + 64 * half + ((uint32_t)((warp & 3) * 32) << 16);
       const uint64_t c2 = pack2(P.scale_log2, P.scale_log2);
       uint64_t sum[2] = {0ull, 0ull};
-      bool ok = true;
       for (int i = 0; i < nb; ++i) {
         const int st = i % PV_STAGES, u = i & 1;
-        ok = mbar_wait(&full[st], (uint32_t)(i / PV_STAGES) & 1u, abort_flag, WD_PAGED | 14u) &&
-             mbar_wait(&s_full[2 * t + u], (uint32_t)(i / 2) & 1u, abort_flag, WD_PAGED | 15u);
-        ok = __all_sync(0xFFFFFFFFu, ok);
-        if (!ok) break;
+        bool ok = mbar_wait(&full[st], (uint32_t)(i / PV_STAGES) & 1u, abort_flag, WD_PAGED | 14u) &&
+                  mbar_wait(&s_full[2 * t + u], (uint32_t)(i / 2) & 1u, abort_flag, WD_PAGED | 15u);
+        if (!__all_sync(0xFFFFFFFFu, ok)) break;
         tc_fence_after();
-        uint32_t sr[4][32];
-#pragma unroll
-        for (int v = 0; v < 4; ++v) tmem_ld_32x32b_x32(ts + 128 * u + 32 * v, sr[v]);
+        uint32_t sr[2][32];
+        tmem_ld_32x32b_x32(ts + 128 * u, sr[0]);
+        tmem_ld_32x32b_x32(ts + 128 * u + 32, sr[1]);
         tmem_ld_wait();
         tc_fence_before();
         __syncwarp();
@@ -617,49 +750,64 @@ __device__ __forceinline__ void sum_weight_tiles(const CUtensorMap& tq, const CU
         const int tok0 = (blk0 + i) * P.tok, pb = p0 + tok0, left = s.n - tok0;
         const bool edge = jt + PT_TILE - 1 > pb || left < P.tok ||
                           (P.window > 0 && pb + P.tok > jt + P.window);
+        const float4* nl = reinterpret_cast<const float4*>(minus_lse[st] + 64 * half);
+        auto add = [&](auto plain) {
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const float4 w = nl[e];
+            const uint32_t* q = &sr[e >> 3][4 * (e & 7)];
+            uint64_t y[2] = {
+                fma2(pack2(__uint_as_float(q[0]), __uint_as_float(q[1])), c2, pack2(w.x, w.y)),
+                fma2(pack2(__uint_as_float(q[2]), __uint_as_float(q[3])), c2, pack2(w.z, w.w))};
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              float a0, a1;
+              if (decltype(plain)::value && (2 * e + x) % 8 == 7) {
+                exp2_pair(y[x], &a0, &a1);
+              } else {
+                unpack2(y[x], &a0, &a1);
+                a0 = exp2_approx(a0);
+                a1 = exp2_approx(a1);
+              }
+              sum[x] = add2(sum[x], pack2(a0, a1));
+            }
+          }
+        };
         if (edge) {
-          const int first = min(max(j - pb, 0), P.tok) * p.G;
+          const int first = min(max(j - pb, 0), P.tok) * p.G - 64 * half;
           int end = min(left, P.tok);
           if (P.window > 0) end = min(end, max(0, j + P.window - pb));
-          const int last = end * p.G;
+          const int last = end * p.G - 64 * half;
 #pragma unroll
-          for (int v = 0; v < 4; ++v)
+          for (int v = 0; v < 2; ++v)
 #pragma unroll
             for (int e = 0; e < 32; ++e)
               if (32 * v + e < first || 32 * v + e >= last) sr[v][e] = 0xFF800000u;
-        }
-        const float4* nl = reinterpret_cast<const float4*>(minus_lse[st]);
-#pragma unroll
-        for (int e = 0; e < 32; ++e) {
-          const float4 w = nl[e];
-          const uint32_t* q = &sr[e >> 3][4 * (e & 7)];
-          const uint64_t ya = fma2(pack2(__uint_as_float(q[0]), __uint_as_float(q[1])), c2, pack2(w.x, w.y));
-          const uint64_t yb = fma2(pack2(__uint_as_float(q[2]), __uint_as_float(q[3])), c2, pack2(w.z, w.w));
-          float a0, a1, b0, b1;
-          unpack2(ya, &a0, &a1);
-          unpack2(yb, &b0, &b1);
-          sum[0] = add2(sum[0], pack2(exp2_approx(a0), exp2_approx(a1)));
-          sum[1] = add2(sum[1], pack2(exp2_approx(b0), exp2_approx(b1)));
+          add(std::false_type());
+        } else {
+          add(std::true_type());
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&empty[st]);
       }
-      if (ok && j >= lo && j < hi) {
-        float a0, a1;
-        unpack2(add2(sum[0], sum[1]), &a0, &a1);
-        P.weights[((long long)b * p.Hkv + g) * P.weights_ld + j] += a0 + a1;
-      }
+      float a0, a1;
+      unpack2(add2(sum[0], sum[1]), &a0, &a1);
+      total = a0 + a1;
     }
+    if (half) half_sum[t * PT_TILE + row] = total;
+    asm volatile("bar.sync 1, 512;" ::: "memory");
+    if (!half && !*abort_flag && j >= lo && j < hi)
+      P.weights[((long long)b * p.Hkv + g) * P.weights_ld + j] += total + half_sum[t * PT_TILE + row];
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 9) {
+  if (warp == PV_SOFT + 1) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
 }
 
-__global__ void __launch_bounds__(PT_THREADS, 1)
+__global__ void __launch_bounds__(PV_THREADS, 1)
     paged_weights_tile_kernel(const __grid_constant__ CUtensorMap tq,
                               const __grid_constant__ CUtensorMap tk,
                               const __grid_constant__ WeightParams P) {
@@ -779,7 +927,7 @@ cudaError_t launch_weight_tiles(const fa_paged_shape& s, const fa_paged_cache& c
   if (e != cudaSuccess) return e;
   const int max_q = s.max_q < s.total_q ? s.max_q : s.total_q;
   const dim3 grid((unsigned)chunk_slots(s, window, PV_KEYS, max_q), (unsigned)s.Hkv, (unsigned)s.B);
-  return launch_overlapped(paged_weights_tile_kernel, grid, PT_THREADS, PV_SMEM, stream, tq, tk, P);
+  return launch_overlapped(paged_weights_tile_kernel, grid, PV_THREADS, PV_SMEM, stream, tq, tk, P);
 }
 
 }  // namespace fa
