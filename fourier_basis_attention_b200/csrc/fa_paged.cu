@@ -27,15 +27,18 @@ constexpr int PR_STAGE = 4 * PR_BOX;        // K and V, two boxes each
 constexpr int PW_STAGES = 3;
 constexpr int PW_STAGE = 2 * PR_BOX;        // K only
 constexpr int PR_OLD = FA_HEAD_DIM + 4;     // fp32 row of the merge buffer
+constexpr int PR_CLUSTER = 8;               // chunks that a cluster merges
 constexpr int PR_RING = PR_WARPS * PR_STAGES * PR_STAGE;
 constexpr int PR_SMEM = PR_RING + 1024;
 constexpr int PW_SMEM = PR_WARPS * PW_STAGES * PW_STAGE + 1024;
-static_assert(PR_WARPS * PR_ROWS * (PR_OLD + 2) * 4 <= PR_RING, "merge buffers fit");
+static_assert(PR_WARPS * PR_ROWS * (PR_OLD + 2) * 4 + PR_ROWS * (FA_HEAD_DIM + 2) * 4 <= PR_RING,
+              "merge buffers fit");
 
 struct RowsParams {
   PagedBatch p;
   int window, tiles, chunk, slots;  // tiles of rows, keys a chunk, partial results a row
   int max_rows;  // sequences of more rows a KV head are another kernel's (0: none are)
+  int cluster;   // the chunks of a tile are one cluster of `slots` CTAs
   float scale_log2;
   const __nv_bfloat16* q;
   long long q_stride;
@@ -68,6 +71,20 @@ __device__ __forceinline__ void ldmatrix_x4_trans(uint32_t (&r)[4], const void* 
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
                : "r"(smem_u32(row)));
 }
+__device__ __forceinline__ float2 ld_cluster_float2(uint32_t addr) {
+  float2 v;
+  asm volatile("ld.shared::cluster.v2.f32 {%0,%1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ float4 ld_cluster_float4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+
 // Byte of element (row, dim) in a block of PR_KEYS rows held as two swizzled 64-dim boxes.
 __device__ __forceinline__ int box_byte(int row, int dim) {
   return (dim >> 6) * PR_BOX + row * 128 + ((((dim & 63) >> 3) ^ (row & 7)) << 4);
@@ -170,7 +187,7 @@ __global__ void __launch_bounds__(PR_THREADS, 3)
   // chunk `slot` of the keys: chunks lie at multiples of P.chunk, the first holds lo
   const int c0 = (lo / P.chunk + slot) * P.chunk;
   const int k_lo = max(lo & ~(PR_KEYS - 1), c0), k_hi = min(hi, c0 + P.chunk);
-  if (k_lo >= k_hi && !(single || (slot == 0 && hi <= lo))) return;  // the merge skips it
+  if (k_lo >= k_hi && !(single || P.cluster || (slot == 0 && hi <= lo))) return;  // the merge skips it
 
   if (threadIdx.x == 0) {
     abort_word = 0;
@@ -300,6 +317,8 @@ __global__ void __launch_bounds__(PR_THREADS, 3)
   __syncthreads();
   float* mo = reinterpret_cast<float*>(smem);
   float2* ml = reinterpret_cast<float2*>(mo + PR_WARPS * PR_ROWS * PR_OLD);
+  float* sum_o = reinterpret_cast<float*>(ml + PR_WARPS * PR_ROWS);  // the CTA's, for its cluster
+  float2* sum_ml = reinterpret_cast<float2*>(sum_o + PR_ROWS * FA_HEAD_DIM);
 #pragma unroll
   for (int u = 0; u < 2; ++u) {
     const int r = (lane >> 2) + 8 * u;
@@ -331,7 +350,10 @@ __global__ void __launch_bounds__(PR_THREADS, 3)
     }
     const long long t = s.q0 + (r0 + r) / p.G;
     const int h = g * p.G + (r0 + r) % p.G;
-    if (single) {
+    if (P.cluster) {
+      *reinterpret_cast<float4*>(sum_o + r * FA_HEAD_DIM + d) = acc;
+      if (d == 0) sum_ml[r] = make_float2(mm, ll);
+    } else if (single) {
       const float inv = ll > 0.0f ? 1.0f / ll : (ll == 0.0f ? 0.0f : ll);
       *reinterpret_cast<uint2*>(P.out + t * P.out_stride + h * FA_HEAD_DIM + d) =
           make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
@@ -342,6 +364,44 @@ __global__ void __launch_bounds__(PR_THREADS, 3)
       if (d == 0) P.part_ml[rec] = make_float2(mm, ll);
     }
   }
+  if (!P.cluster) return;
+  // the cluster's CTAs (rank = slot) take every slots-th row each and read all CTAs' sums of it
+  cluster_sync_all();
+  for (int r = slot + P.slots * warp; r < rows; r += P.slots * PR_WARPS) {
+    const uint32_t ao = smem_u32(sum_o + r * FA_HEAD_DIM + 4 * lane), am = smem_u32(sum_ml + r);
+    float2 e[PR_CLUSTER];
+    float4 x[PR_CLUSTER];
+    float mm = -INFINITY;
+#pragma unroll
+    for (int k = 0; k < PR_CLUSTER; ++k) {
+      e[k] = make_float2(-INFINITY, 0.0f);
+      x[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      if (k < P.slots) {
+        e[k] = ld_cluster_float2(mapa_shared(am, k));
+        x[k] = ld_cluster_float4(mapa_shared(ao, k));
+      }
+      mm = fmaxf(mm, e[k].x);
+    }
+    const float base = mm == -INFINITY ? 0.0f : mm;
+    float ll = 0.0f;
+    float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+    for (int k = 0; k < PR_CLUSTER; ++k) {
+      const float f = exp2_approx(e[k].x - base);
+      ll = fmaf(e[k].y, f, ll);
+      acc.x = fmaf(x[k].x, f, acc.x);
+      acc.y = fmaf(x[k].y, f, acc.y);
+      acc.z = fmaf(x[k].z, f, acc.z);
+      acc.w = fmaf(x[k].w, f, acc.w);
+    }
+    const long long t = s.q0 + (r0 + r) / p.G;
+    const int h = g * p.G + (r0 + r) % p.G;
+    const float inv = ll > 0.0f ? 1.0f / ll : (ll == 0.0f ? 0.0f : ll);
+    *reinterpret_cast<uint2*>(P.out + t * P.out_stride + h * FA_HEAD_DIM + 4 * lane) =
+        make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
+    if (lane == 0 && P.lse) P.lse[t * p.Hq + h] = 0.693147180559945309f * (mm + log2f(ll));
+  }
+  cluster_sync_all();  // the CTA's shared memory is read no more
 }
 
 struct JoinParams {
@@ -626,8 +686,19 @@ static cudaError_t attend_plan(const fa_paged_shape& s, int window, AttendPlan* 
   P->chunk = rows_chunk(s, P->tiles, 32 * sms);
   P->slots = chunk_slots(s, window, P->chunk, (PR_ROWS + G - 1) / G);
   P->window = window;
+  // Caches of at most 4096 tokens go in 8 chunks of at least 64 tokens that one cluster merges:
+  // the second kernel takes longer than such a chunk.
+  if (P->max_rows > 0 && s.max_kv <= PR_CLUSTER * 512 && P->slots > 1) {
+    const int c = ((s.max_kv + PR_CLUSTER - 1) / PR_CLUSTER + 63) / 64 * 64;
+    const int n = chunk_slots(s, window, c, (PR_ROWS + G - 1) / G);
+    if (n <= PR_CLUSTER) {
+      P->chunk = c;
+      P->slots = n;
+      P->cluster = n > 1;
+    }
+  }
   a->rows_records = 0;
-  if (P->slots > 1)
+  if (P->slots > 1 && !P->cluster)
     a->rows_records = (P->max_rows > 0 ? (size_t)s.B * s.Hkv * PR_ROWS : (size_t)s.total_q * s.Hq) * P->slots;
   *bytes = (a->rows_records + a->t.records) * (FA_HEAD_DIM * sizeof(float) + sizeof(float2));
   return cudaSuccess;
@@ -666,8 +737,19 @@ cudaError_t launch_paged_attend(const fa_paged_shape& s, const fa_paged_cache& c
   if ((e = raise_smem_limit(reinterpret_cast<const void*>(paged_rows_kernel), PR_SMEM)) != cudaSuccess)
     return e;
   const dim3 grid((unsigned)(P.slots * P.tiles), (unsigned)s.Hkv, (unsigned)s.B);
-  paged_rows_kernel<<<grid, PR_THREADS, PR_SMEM, stream>>>(tk, tv, P);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(PR_THREADS, 1, 1);
+  cfg.dynamicSmemBytes = PR_SMEM;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = P.cluster ? (unsigned)P.slots : 1u;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if ((e = cudaLaunchKernelEx(&cfg, paged_rows_kernel, tk, tv, P)) != cudaSuccess) return e;
   float* tile_o = part_o + a.rows_records * FA_HEAD_DIM;
   float2* tile_ml = part_ml + a.rows_records;
   if (a.t.tok > 0 &&
@@ -693,7 +775,7 @@ cudaError_t launch_paged_attend(const fa_paged_shape& s, const fa_paged_cache& c
     const long long rows = max_rows > 0 ? (long long)s.B * s.Hkv * max_rows : (long long)s.total_q * s.Hq;
     return launch_overlapped(paged_join_kernel, dim3((unsigned)((rows + 7) / 8)), 256, 0, stream, J);
   };
-  if (P.slots > 1 &&
+  if (P.slots > 1 && !P.cluster &&
       (e = join(P.chunk, P.slots, PR_ROWS, P.max_rows, 0, part_o, part_ml)) != cudaSuccess)
     return e;
   if (a.t.slots > 1) e = join(a.t.chunk, a.t.slots, 2 * a.t.tok * P.p.G, 0, PR_ROWS, tile_o, tile_ml);
