@@ -39,6 +39,9 @@ struct TileShared {
 };
 constexpr int PT_SMEM = (2 + PT_STAGES) * PT_BLOCK + (int)sizeof(TileShared);
 static_assert(PT_SMEM <= 232448, "fits the SM");
+// Registers after setmaxnreg, a thread: the two sums must not pass what the launch gives the
+// block, or the raise waits for good (launches check it).
+constexpr int PT_REGS = PT_SOFT * 32 * 208 + 4 * 32 * 88;
 constexpr float PT_SLACK = 8.0f;              // log2 by which the maximum may pass m
 
 struct TileParams {
@@ -558,6 +561,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1)
 // key) against one exp2: 512 and 1024 clocks for a 128 x 128 tile.
 constexpr int PV_SOFT = 16;                   // warps that sum; 4 more as above
 constexpr int PV_THREADS = (PV_SOFT + 4) * 32;
+constexpr int PV_REGS = PV_SOFT * 32 * 104 + 4 * 32 * 64;
 constexpr int PV_STAGES = 4;
 constexpr int PV_KEYS = 2 * PT_TILE;
 constexpr int PV_SMEM = (2 + PV_STAGES) * PT_BLOCK + 1024;
@@ -832,6 +836,17 @@ bool encode_queries(CUtensorMap* map, const void* q, const fa_paged_shape& s, in
                 CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+static cudaError_t prepare_kernel(const void* fn, int smem, int threads, int regs, const char** why) {
+  cudaFuncAttributes at;
+  cudaError_t e = cudaFuncGetAttributes(&at, fn);
+  if (e != cudaSuccess) return e;
+  if (at.numRegs * threads < regs) {
+    *why = "the kernel was built with fewer registers than its warps share out";
+    return cudaErrorInvalidConfiguration;
+  }
+  return raise_smem_limit(fn, smem);
+}
+
 // Key rows of a TMA box: the largest power of two, at most a block, that divides a page (so
 // that no box crosses its end); a whole block where a sequence has one page.
 int key_box(const fa_paged_shape& s) {
@@ -896,7 +911,7 @@ cudaError_t launch_tiles(const fa_paged_shape& s, const fa_paged_cache& c, const
     return cudaErrorInvalidValue;
   }
   const void* fn = reinterpret_cast<const void*>(paged_tile_kernel);
-  cudaError_t e = raise_smem_limit(fn, PT_SMEM);
+  cudaError_t e = prepare_kernel(fn, PT_SMEM, PT_THREADS, PT_REGS, why);
   if (e != cudaSuccess) return e;
   const long long ctas = (long long)t.tiles * t.slots * s.Hkv;
   return launch_overlapped(paged_tile_kernel, dim3((unsigned)ctas), PT_THREADS, PT_SMEM, stream, tq, tk, tv, P);
@@ -923,7 +938,7 @@ cudaError_t launch_weight_tiles(const fa_paged_shape& s, const fa_paged_cache& c
     return cudaErrorInvalidValue;
   }
   const void* fn = reinterpret_cast<const void*>(paged_weights_tile_kernel);
-  cudaError_t e = raise_smem_limit(fn, PV_SMEM);
+  cudaError_t e = prepare_kernel(fn, PV_SMEM, PV_THREADS, PV_REGS, why);
   if (e != cudaSuccess) return e;
   const int max_q = s.max_q < s.total_q ? s.max_q : s.total_q;
   const dim3 grid((unsigned)chunk_slots(s, window, PV_KEYS, max_q), (unsigned)s.Hkv, (unsigned)s.B);

@@ -123,6 +123,15 @@ CASES = {
     "window_wide": ([(50, 90), (1, 33)], 4, 4, 16, 100000),
     "window_int_max": ([(50, 90), (1, 33)], 4, 4, 16, 2 ** 31 - 1),
     "many_short": ([(1 + i % 3, 1 + (37 * i) % 90) for i in range(40)], 4, 2, 16, 0),
+    "not_cached": ([(40, 0), (30, 10), (17, 3), (1, 0)], 8, 2, 16, 0),
+    "not_cached_window": ([(60, 0), (50, 20), (5, 2)], 8, 2, 16, 7),
+    "g100": ([(1, 300), (9, 200)], 100, 1, 16, 0),
+    "g128": ([(1, 60), (7, 200), (2, 1100)], 128, 1, 16, 0),
+    "g200": ([(1, 100), (3, 40)], 200, 1, 16, 9),
+    "many_chunks": ([(5 + i % 40, 60 + (91 * i) % 300) for i in range(70)], 4, 1, 16, 0),
+    "decode_over_4096": ([(1, 9001), (2, 4200), (1, 5)], 8, 2, 64, 0),
+    "decode_4096": ([(1, 4096), (1, 1), (2, 513), (0, 9)], 8, 2, 128, 0),
+    "decode_4096_window": ([(1, 4096), (3, 700), (1, 1)], 4, 1, 64, 600),
     "mixed": ([(1, 1800), (140, 900), (1, 3), (260, 1500), (2, 1200)], 16, 4, 64, 0),
 }
 
@@ -474,8 +483,9 @@ def check_evict(st, w, keep, sink, recent, dst_page, with_weights=True):
     ([1025, 1024, 1023], 1, 1024, 0, 0, 1024),
     ([300, 299], 7, 299, 299, 0, 64),
     ([2000, 3], 48, 50, 0, 50, 16),
-    ([40000], 128, 5001, 31, 777, 64)],
-    ids=["one", "short", "ragged", "borders", "all_sink", "all_recent", "long"])
+    ([40000], 128, 5001, 31, 777, 64),
+    ([200000, 9], 128, 150, 3, 50, 64)],
+    ids=["one", "short", "ragged", "borders", "all_sink", "all_recent", "long", "read_again"])
 @pytest.mark.parametrize("kind", ["random", "ties", "special"])
 def test_evict(kvs, page, keep, sink, recent, dst_page, kind):
     st = make([(0, kv) for kv in kvs], 4, 2, page, seed=21, fill=0.0)
@@ -536,6 +546,76 @@ def test_evict_into_dense_then_compress():
     scale = dec.abs().max().item()
     # both round to bf16 once or twice; fa_decode's own bound is 3e-3 of the largest value
     assert (again.float() - dec).abs().max().item() <= (3e-3 + 2 * U16) * scale
+
+
+def test_pools_of_more_than_2_31_elements():
+    """Pages at both ends of pools of 2.6e9 elements: write, attention, weights, eviction."""
+    page, pages = 128, 160000
+    K = torch.empty(pages, 1, page, D, dtype=BF, device="cuda")
+    V = torch.empty_like(K)
+    table = torch.tensor([[pages - 1, 0, pages - 2]], dtype=torch.int32, device="cuda")
+    cache = fa.PagedCache(K, V, table)
+    n, Hq = 300, 4
+    gen = torch.Generator().manual_seed(7)
+    k, v, q = (torch.randn(n, h, D, generator=gen).to(BF).cuda() for h in (1, 1, Hq))
+    batch = fa.PagedBatch(cache, Hq, torch.tensor([0, n], dtype=torch.int32, device="cuda"),
+                          torch.tensor([n], dtype=torch.int32, device="cuda"), total_q=n, max_q=n, max_kv=n)
+    fa.fa_paged_append(batch, k, v)
+    small = fa.PagedCache(K[[pages - 1, 0, pages - 2]].contiguous(), V[[pages - 1, 0, pages - 2]].contiguous(),
+                          torch.tensor([[0, 1, 2]], dtype=torch.int32, device="cuda"))
+    rows = small.K[:, 0].reshape(-1, D)
+    assert torch.equal(rows[:n], k[:, 0]) and torch.equal(small.V[:, 0].reshape(-1, D)[:n], v[:, 0])
+    st = dict(K=small.K, V=small.V, table=small.page_table, q=q, used=n, total=n, batch=batch,
+              q_start=batch.q_start, kv_len=batch.kv_len)
+    out, lse = attend(st)
+    check_attend(st, out, lse, reference(st))
+    first = fa.PagedBatch(cache, Hq, torch.tensor([0, 1], dtype=torch.int32, device="cuda"), batch.kv_len,
+                          total_q=1, max_q=1, max_kv=n)
+    st1 = dict(st, q=q[-1:], used=1, total=1, batch=first, q_start=first.q_start)
+    out, lse = attend(st1)
+    check_attend(st1, out, lse, reference(st1))
+    acc = torch.zeros(1, 1, n, device="cuda")
+    fa.fa_paged_weights(first, q[-1:], lse, acc)
+    w = reference(st1)[4]
+    assert (np.abs(acc.double().cpu().numpy() - w) <= 1e-3 * w + 1e-30).all()
+    far = fa.PagedCache(K, V, torch.tensor([[pages - 3]], dtype=torch.int32, device="cuda"))
+    index = torch.empty(1, 1, 100, dtype=torch.int32, device="cuda")
+    length = torch.empty(1, dtype=torch.int32, device="cuda")
+    fa.fa_evict(batch, acc, 100, far, index, length, recent=10)
+    fa.fa_device_status()
+    assert torch.equal(K[pages - 3, 0, :100], k[index[0, 0].long(), 0])
+
+
+def test_first_call_of_a_process_is_captured():
+    """Nothing of a first call (module load, limits, tensor maps) breaks a capture."""
+    code = ("import sys, torch; sys.path.insert(0, %r)\n"
+            "import fourier_basis_attention_b200 as fa\n"
+            "bf, i32 = torch.bfloat16, torch.int32\n"
+            "K = torch.randn(4, 2, 64, 128, device='cuda').to(bf)\n"
+            "c = fa.PagedCache(K, K.clone(), torch.arange(4, dtype=i32, device='cuda').view(2, 2))\n"
+            "q = torch.randn(41, 8, 128, device='cuda').to(bf)\n"
+            "b = fa.PagedBatch(c, 8, torch.tensor([0, 40, 41], dtype=i32, device='cuda'),\n"
+            "                  torch.tensor([100, 90], dtype=i32, device='cuda'), 41, 40, 128)\n"
+            "out, lse, acc = torch.empty_like(q), torch.empty(41, 8, device='cuda'), torch.zeros(2, 2, 128, device='cuda')\n"
+            "ws = torch.empty(max(16, fa.fa_paged_attend_workspace_size(b)), dtype=torch.uint8, device='cuda')\n"
+            "d = fa.PagedCache.dense(torch.zeros(2, 2, 32, 128, dtype=bf, device='cuda'), torch.zeros(2, 2, 32, 128, dtype=bf, device='cuda'))\n"
+            "i, n = torch.zeros(2, 2, 32, dtype=i32, device='cuda'), torch.zeros(2, dtype=i32, device='cuda')\n"
+            "r = fa.fa_rope_init()\n"
+            "def go():\n"
+            "    fa.fa_paged_append(b, q[:, :2], q[:, 2:4], q=q, q_out=out, rope=r)\n"
+            "    fa.fa_rope(r, q[None], pos, q2[None])\n"
+            "    fa.fa_paged_attend(b, q, out, ws, lse=lse)\n"
+            "    fa.fa_paged_weights(b, q, lse, acc)\n"
+            "    fa.fa_evict(b, acc, 32, d, i, n)\n"
+            "pos, q2 = torch.zeros(1, 41, dtype=i32, device='cuda'), torch.empty_like(q)\n"
+            "torch.cuda.synchronize()\n"
+            "g = torch.cuda.CUDAGraph()\n"
+            "with torch.cuda.graph(g): go()\n"
+            "acc.zero_(); g.replay(); torch.cuda.synchronize(); fa.fa_device_status()\n"
+            "a = [t.clone() for t in (out, lse, acc, i, n, q2)]\n"
+            "acc.zero_(); go(); fa.fa_device_status()\n"
+            "assert all(torch.equal(x, y) for x, y in zip(a, (out, lse, acc, i, n, q2)))\n") % ROOT
+    subprocess.run([sys.executable, "-c", code], check=True, timeout=120)
 
 
 # --------------------------------------------------------------------------- a run of them together
