@@ -97,6 +97,8 @@ int check_softmax(const fa_paged_shape& s, float* scale, int32_t* window) {
                 s.page_size, s.max_kv);
   if (!isfinite(*scale) || *scale < 0.0f)
     return fail(FA_ERR_INVALID, "scale must be finite and >= 0");
+  if (*scale != 0.0f && (*scale < 1e-20f || *scale > 1e20f))
+    return fail(FA_ERR_UNSUPPORTED, "scale=%g is outside [1e-20, 1e20]", *scale);
   if (*window < 0) return fail(FA_ERR_INVALID, "window=%d is negative", *window);
   if (*window >= s.max_kv) *window = 0;  // hides nothing
   if (*scale == 0.0f) *scale = 0.08838834764831845f;  // 1 / sqrt(128)

@@ -84,6 +84,11 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
   return r;
 }
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
 __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   uint64_t r;
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
@@ -106,13 +111,14 @@ constexpr uint32_t PT_DESC_HI = (1024u >> 4) | (1u << 14) | (2u << 29);
 __device__ __forceinline__ uint32_t desc_lo(uint32_t addr, uint32_t lbo) {
   return (addr >> 4) | ((lbo >> 4) << 16);
 }
-__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t idesc, bool add) {
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t idesc, bool add,
+                                       uint32_t hi = PT_DESC_HI) {
   asm volatile(
       "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
       "setp.ne.b32 p, %5, 0;\n\t"
       "mov.b64 a, {%1, %3};\n\tmov.b64 b, {%2, %3};\n\t"
       "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, p;\n\t}" ::"r"(d),
-      "r"(a_lo), "r"(b_lo), "r"(PT_DESC_HI), "r"(idesc), "r"((uint32_t)add)
+      "r"(a_lo), "r"(b_lo), "r"(hi), "r"(idesc), "r"((uint32_t)add)
       : "memory");
 }
 __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a_tmem, uint32_t b_lo, uint32_t idesc, bool add) {
@@ -555,21 +561,27 @@ __global__ void __launch_bounds__(PT_THREADS, 1)
 
 // Weights that keys gather: w_j += sum_rows exp2(c s_rj - log2 e lse_r). A CTA keeps 256 keys
 // (two tiles) and streams the query rows that see them in blocks of 128, as S^T = K Q^T: a
-// thread owns a key (a lane of tensor memory) and sums along its columns, so that nothing is
-// reduced across threads and a key's sum is taken in one order. Scores are double-buffered:
-// the tensor core writes one buffer while the other is summed. Bound: 2 * 128 flops a (row,
-// key) against one exp2: 512 and 1024 clocks for a 128 x 128 tile.
+// thread owns a key (a lane of tensor memory) and sums along half its columns, so that nothing
+// is reduced across threads but the two halves and a key's sum is taken in one order. Scores are
+// double-buffered: the tensor core writes one buffer while the other is summed.
+//   -lse / scale joins the product as 16 more dims: the keys hold 1, 1, 1, 0, ..., a row its
+// value in three bf16 parts (exact to 2^-24 of it, as an fp32 product would be). Read from shared
+// memory by every thread for every column it took as many cycles as the exponentials.
+//   Bound: 2 * 144 flops a (row, key) against one exp2: 576 and 1024 clocks for a 128 x 128 tile.
 constexpr int PV_SOFT = 16;                   // warps that sum; 4 more as above
 constexpr int PV_THREADS = (PV_SOFT + 4) * 32;
 constexpr int PV_REGS = PV_SOFT * 32 * 104 + 4 * 32 * 64;
 constexpr int PV_STAGES = 4;
 constexpr int PV_KEYS = 2 * PT_TILE;
-constexpr int PV_SMEM = (2 + PV_STAGES) * PT_BLOCK + 1024;
+// 16 more dims of 128 rows, unswizzled: 8 rows x 8 dims contiguous, 16 such, then the other dims
+constexpr int PV_EXTRA = PT_TILE * 32;
+constexpr uint32_t PV_EXTRA_HI = (128u >> 4) | (1u << 14);
+constexpr int PV_SMEM = (2 + PV_STAGES) * PT_BLOCK + (1 + PV_STAGES) * PV_EXTRA + 1024;
 
 struct WeightParams {
   PagedBatch p;
   int window, tok, box, skip_rows;
-  float scale_log2;
+  float scale_log2, inv_scale;
   const float* lse;
   float* weights;
   long long weights_ld;
@@ -581,8 +593,9 @@ __device__ __forceinline__ void sum_weight_tiles(const CUtensorMap& tq, const CU
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
   uint8_t* ring = smem + 2 * PT_BLOCK;
+  uint8_t* ones = ring + PV_STAGES * PT_BLOCK;  // the keys' extra dims
+  uint8_t* extra = ones + PV_EXTRA;             // [stage] the rows'
   __shared__ uint64_t full[PV_STAGES], empty[PV_STAGES], k_full, s_full[4], s_empty[4], drained;
-  __shared__ __align__(16) float minus_lse[PV_STAGES][PT_TILE];
   __shared__ float half_sum[PV_KEYS];
   __shared__ uint32_t tmem_ptr;
   __shared__ int abort_word;
@@ -606,7 +619,7 @@ __device__ __forceinline__ void sum_weight_tiles(const CUtensorMap& tq, const CU
     abort_word = 0;
     for (int i = 0; i < PV_STAGES; ++i) {
       mbar_init(&full[i], 2);
-      mbar_init(&empty[i], 1 + 8 * (1 + two));
+      mbar_init(&empty[i], 1);
     }
     mbar_init(&k_full, 1);
     mbar_init(&drained, 1);
@@ -626,6 +639,9 @@ __device__ __forceinline__ void sum_weight_tiles(const CUtensorMap& tq, const CU
     const int pad = PT_TILE - P.tok * p.G, r = PT_TILE - 1 - w / 8 % pad, h = w / 8 / pad;
     *reinterpret_cast<uint4*>(ring + h * PT_HALF + r * 128 + (w & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
   }
+  for (int w = threadIdx.x; w < (1 + PV_STAGES) * PV_EXTRA / 16; w += PV_THREADS)
+    reinterpret_cast<uint4*>(ones)[w] =
+        w < PT_TILE ? make_uint4(0x3F803F80u, 0x3F80u, 0u, 0u) : make_uint4(0u, 0u, 0u, 0u);
   fence_proxy_async_smem();
   __syncthreads();
   tc_fence_after();
@@ -666,6 +682,7 @@ __device__ __forceinline__ void sum_weight_tiles(const CUtensorMap& tq, const CU
       // ---------------------------------------------------------------- MMA
       constexpr uint32_t id = idesc_bf16_f32(PT_TILE, PT_TILE, false);
       const uint32_t a_lo = desc_lo(smem_u32(smem), 16), b_lo = desc_lo(smem_u32(ring), 16);
+      const uint32_t one_lo = desc_lo(smem_u32(ones), PV_EXTRA / 2), x_lo = desc_lo(smem_u32(extra), PV_EXTRA / 2);
       bool ok = mbar_wait(&k_full, 0, abort_flag, WD_PAGED | 10u);
       for (int i = 0; i < nb; ++i) {
         const int st = i % PV_STAGES, u = i & 1;
@@ -683,6 +700,7 @@ __device__ __forceinline__ void sum_weight_tiles(const CUtensorMap& tq, const CU
               mma_ss(tmem + 128 * (2 * t + u), a_lo + t * (PT_BLOCK >> 4) + off,
                      b_lo + st * (PT_BLOCK >> 4) + off, id, k > 0);
             }
+            mma_ss(tmem + 128 * (2 * t + u), one_lo, x_lo + st * (PV_EXTRA >> 4), id, true, PV_EXTRA_HI);
             mma_commit(&s_full[2 * t + u]);
             if (t == two) mma_commit(&empty[st]);
           }
@@ -702,26 +720,36 @@ __device__ __forceinline__ void sum_weight_tiles(const CUtensorMap& tq, const CU
       auto load = [&](int i, float (&e)[4]) {
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
-          const int col = 4 * lane + x, tok = (blk0 + i) * P.tok + col / p.G;
-          e[x] = INFINITY;  // columns without a row add nothing
-          if (i < nb && col < P.tok * p.G && tok < s.n)
-            e[x] = P.lse[(long long)(s.q0 + tok) * p.Hq + g * p.G + col % p.G];
+          const int row = lane + 32 * x, tok = (blk0 + i) * P.tok + row / p.G;
+          e[x] = -INFINITY;
+          if (i < nb && row < P.tok * p.G && tok < s.n)
+            e[x] = P.lse[(long long)(s.q0 + tok) * p.Hq + g * p.G + row % p.G];
         }
       };
       float next[4];
       load(0, next);
       for (int i = 0; i < nb; ++i) {
         const int st = i % PV_STAGES;
-        float e[4];
+        uint4 e[4];
 #pragma unroll
-        for (int x = 0; x < 4; ++x)  // nor do rows that see no key
-          e[x] = next[x] == -INFINITY ? -INFINITY : -1.44269504088896341f * next[x];
+        for (int x = 0; x < 4; ++x) {
+          // columns without a row, and rows that see no key, add nothing
+          const float v = next[x] == -INFINITY ? -3e38f : -next[x] * P.inv_scale;
+          const __nv_bfloat16 a = __float2bfloat16_rn(v);
+          const float r = v - __bfloat162float(a);
+          const __nv_bfloat16 b = __float2bfloat16_rn(r);
+          e[x] = make_uint4(__bfloat16_as_ushort(a) | (uint32_t)__bfloat16_as_ushort(b) << 16,
+                            __bfloat16_as_ushort(__float2bfloat16_rn(r - __bfloat162float(b))), 0u, 0u);
+        }
         load(i + 1, next);
         bool ok = true;
         if (i >= PV_STAGES)
           ok = mbar_wait(&empty[st], (uint32_t)(i / PV_STAGES - 1) & 1u, abort_flag, WD_PAGED | 13u);
         if (!__all_sync(0xFFFFFFFFu, ok)) break;
-        *reinterpret_cast<float4*>(&minus_lse[st][4 * lane]) = make_float4(e[0], e[1], e[2], e[3]);
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+          reinterpret_cast<uint4*>(extra + st * PV_EXTRA)[lane + 32 * x] = e[x];
+        fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&full[st]);
       }
@@ -738,9 +766,8 @@ __device__ __forceinline__ void sum_weight_tiles(const CUtensorMap& tq, const CU
       const uint64_t c2 = pack2(P.scale_log2, P.scale_log2);
       uint64_t sum[2] = {0ull, 0ull};
       for (int i = 0; i < nb; ++i) {
-        const int st = i % PV_STAGES, u = i & 1;
-        bool ok = mbar_wait(&full[st], (uint32_t)(i / PV_STAGES) & 1u, abort_flag, WD_PAGED | 14u) &&
-                  mbar_wait(&s_full[2 * t + u], (uint32_t)(i / 2) & 1u, abort_flag, WD_PAGED | 15u);
+        const int u = i & 1;
+        const bool ok = mbar_wait(&s_full[2 * t + u], (uint32_t)(i / 2) & 1u, abort_flag, WD_PAGED | 15u);
         if (!__all_sync(0xFFFFFFFFu, ok)) break;
         tc_fence_after();
         uint32_t sr[2][32];
@@ -754,27 +781,20 @@ __device__ __forceinline__ void sum_weight_tiles(const CUtensorMap& tq, const CU
         const int tok0 = (blk0 + i) * P.tok, pb = p0 + tok0, left = s.n - tok0;
         const bool edge = jt + PT_TILE - 1 > pb || left < P.tok ||
                           (P.window > 0 && pb + P.tok > jt + P.window);
-        const float4* nl = reinterpret_cast<const float4*>(minus_lse[st] + 64 * half);
         auto add = [&](auto plain) {
 #pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            const float4 w = nl[e];
-            const uint32_t* q = &sr[e >> 3][4 * (e & 7)];
-            uint64_t y[2] = {
-                fma2(pack2(__uint_as_float(q[0]), __uint_as_float(q[1])), c2, pack2(w.x, w.y)),
-                fma2(pack2(__uint_as_float(q[2]), __uint_as_float(q[3])), c2, pack2(w.z, w.w))};
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-              float a0, a1;
-              if (decltype(plain)::value && (2 * e + x) % 8 == 7) {
-                exp2_pair(y[x], &a0, &a1);
-              } else {
-                unpack2(y[x], &a0, &a1);
-                a0 = exp2_approx(a0);
-                a1 = exp2_approx(a1);
-              }
-              sum[x] = add2(sum[x], pack2(a0, a1));
+          for (int e = 0; e < 32; ++e) {
+            const uint32_t* q = &sr[e >> 4][2 * (e & 15)];
+            const uint64_t y = mul2(pack2(__uint_as_float(q[0]), __uint_as_float(q[1])), c2);
+            float a0, a1;
+            if (decltype(plain)::value && e % 4 == 3) {
+              exp2_pair(y, &a0, &a1);
+            } else {
+              unpack2(y, &a0, &a1);
+              a0 = exp2_approx(a0);
+              a1 = exp2_approx(a1);
             }
+            sum[e & 1] = add2(sum[e & 1], pack2(a0, a1));
           }
         };
         if (edge) {
@@ -791,8 +811,6 @@ __device__ __forceinline__ void sum_weight_tiles(const CUtensorMap& tq, const CU
         } else {
           add(std::true_type());
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&empty[st]);
       }
       float a0, a1;
       unpack2(add2(sum[0], sum[1]), &a0, &a1);
@@ -929,6 +947,7 @@ cudaError_t launch_weight_tiles(const fa_paged_shape& s, const fa_paged_cache& c
   P.box = key_box(s);
   P.skip_rows = skip_rows;
   P.scale_log2 = scale * 1.44269504088896341f;
+  P.inv_scale = 1.0f / scale;
   P.lse = lse;
   P.weights = weights;
   P.weights_ld = weights_ld;

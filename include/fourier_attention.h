@@ -477,7 +477,7 @@ int fa_paged_append(const fa_paged_shape* shape, const fa_paged_cache* cache,
  * batch.
  *   q        device bf16 [total_q][Hq][128], token stride q_stride (a multiple of 8,
  *            >= Hq * 128).
- *   scale    softmax scale, finite and >= 0; 0 picks 1/sqrt(128).
+ *   scale    softmax scale, 0 (picks 1/sqrt(128)) or 1e-20 to 1e20.
  *   window   0: the token at cache index p sees keys j <= p; > 0: p - window < j <= p.
  *   out      device bf16 [total_q][Hq][128], token stride out_stride.
  *   lse      device fp32 [total_q][Hq] or NULL: log of the sum of exp(score), the scores

@@ -193,7 +193,8 @@ def test_bad_caches(name, kw):
     ("fa_paged_attend", dict(q=None), 1), ("fa_paged_attend", dict(out=None), 1), ("fa_paged_attend", dict(qs=1016), 1),
     ("fa_paged_attend", dict(os=1028), 1), ("fa_paged_attend", dict(lse=P + 2), 1),
     ("fa_paged_attend", dict(scale=-1.0), 1), ("fa_paged_attend", dict(scale=math.nan), 1),
-    ("fa_paged_attend", dict(scale=math.inf), 1), ("fa_paged_attend", dict(window=-1), 1),
+    ("fa_paged_attend", dict(scale=math.inf), 1), ("fa_paged_attend", dict(scale=1e-30), 2),
+    ("fa_paged_weights", dict(scale=1e30), 2), ("fa_paged_attend", dict(window=-1), 1),
     ("fa_paged_attend", dict(shape=shape_of(page_size=20, max_kv=300)), 2),
     ("fa_paged_weights", dict(q=P + 8), 1), ("fa_paged_weights", dict(lse=None), 1),
     ("fa_paged_weights", dict(w=None), 1), ("fa_paged_weights", dict(ld=319), 1),
