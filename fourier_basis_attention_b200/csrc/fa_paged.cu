@@ -409,6 +409,7 @@ struct JoinParams {
   int window, chunk, slots;
   int tile_rows;           // rows whose keys were split together
   int max_rows, min_rows;  // as RowsParams::max_rows; rows of a sequence must exceed min_rows
+  int rows;                // rows a sequence and KV head may have, where max_rows is set
   const float* part_o;
   const float2* part_ml;
   __nv_bfloat16* out;
@@ -416,24 +417,30 @@ struct JoinParams {
   float* lse;
 };
 
-// Joins the chunks of each row: one warp a row, chunks in order.
+// Joins the chunks of each row. SPLIT warps a row, every SPLIT-th chunk each, then the warps in
+// order: 8 where rows are few and chunks may be many (one token over 30000 keys in 118 chunks: 48
+// us with one warp a row, 35 with 8), 1 where there are thousands of rows (a chunk of 100 tokens:
+// 30 us with 8, 23 with 1; 64 decode tokens: 338 and 325).
+template <int SPLIT>
 __global__ void __launch_bounds__(256) paged_join_kernel(const __grid_constant__ JoinParams P) {
+  __shared__ float4 part[SPLIT][32];
+  __shared__ float2 part_ml[SPLIT];
   const PagedBatch& p = P.p;
-  const int lane = threadIdx.x & 31;
-  const long long row = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) % SPLIT;
+  const long long at = (long long)blockIdx.x * (8 / SPLIT) + (threadIdx.x >> 5) / SPLIT;
   int b = 0, r = 0, g = 0;  // sequence, row of it in its KV head
   SeqSpan s;
   bool live = false;
   if (P.max_rows > 0) {
-    r = (int)(row % P.max_rows);
-    g = (int)(row / P.max_rows % p.Hkv);
-    b = (int)(row / P.max_rows / p.Hkv);
+    r = (int)(at % P.rows);
+    g = (int)(at / P.rows % p.Hkv);
+    b = (int)(at / P.rows / p.Hkv);
     if (b < p.B) {
       s = seq_span(p, b);
       live = r < s.n * p.G && s.n * p.G <= P.max_rows;
     }
   } else {
-    const int t = (int)(row / p.Hq), h = (int)(row % p.Hq);
+    const int t = (int)(at / p.Hq), h = (int)(at % p.Hq);
     for (int b0 = 0; b0 < p.B; b0 += 32) {
       const int i = b0 + lane + 1;
       const int n = __popc(__ballot_sync(0xFFFFFFFFu, i <= p.B && p.q_start[i] <= t));
@@ -449,43 +456,36 @@ __global__ void __launch_bounds__(256) paged_join_kernel(const __grid_constant__
   }
   wait_earlier_kernel();
   if (!live) return;
-  const int tile = r / P.tile_rows;
+  const int tile = r / P.tile_rows;  // rows whose keys were split together
   int lo, hi;
   row_keys(s, p.G, P.window, tile * P.tile_rows, min((tile + 1) * P.tile_rows, s.n * p.G), &lo, &hi);
   const int slots = hi > lo ? (hi - 1) / P.chunk - lo / P.chunk + 1 : 1;
+  const long long t = s.q0 + r / p.G;
+  const int h = g * p.G + r % p.G;
+  const long long row = part_row(p, P.max_rows, b, g, t, h, r);
   const float2* ml = P.part_ml + row * P.slots;
   const float4* po = reinterpret_cast<const float4*>(P.part_o + row * P.slots * FA_HEAD_DIM) + lane;
   float mm = -INFINITY, ll = 0.0f;
   float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-  for (int k0 = 0; k0 < slots; k0 += 32) {  // lane k: chunk k0 + k
-    const float2 e = k0 + lane < slots ? ml[k0 + lane] : make_float2(-INFINITY, 0.0f);
-    float top = fmaxf(mm, e.x);
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
-    const float base = top == -INFINITY ? 0.0f : top;
+  auto add = [&](const float2& e, const float4& x) {
+    const float top = fmaxf(mm, e.x), base = top == -INFINITY ? 0.0f : top;
     const float f = exp2_approx(mm - base), fe = exp2_approx(e.x - base);
     mm = top;
-    float l = e.y * fe;
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, d);
-    ll = ll * f + l;
-    acc.x *= f;
-    acc.y *= f;
-    acc.z *= f;
-    acc.w *= f;
-    const int n = min(32, slots - k0);
-#pragma unroll 8
-    for (int k = 0; k < n; ++k) {
-      const float4 x = po[(k0 + k) * (FA_HEAD_DIM / 4)];
-      const float w = __shfl_sync(0xFFFFFFFFu, fe, k);
-      acc.x = fmaf(w, x.x, acc.x);
-      acc.y = fmaf(w, x.y, acc.y);
-      acc.z = fmaf(w, x.z, acc.z);
-      acc.w = fmaf(w, x.w, acc.w);
-    }
+    ll = ll * f + e.y * fe;
+    acc.x = acc.x * f + x.x * fe;
+    acc.y = acc.y * f + x.y * fe;
+    acc.z = acc.z * f + x.z * fe;
+    acc.w = acc.w * f + x.w * fe;
+  };
+#pragma unroll 4
+  for (int k = warp; k < slots; k += SPLIT) add(ml[k], po[k * (FA_HEAD_DIM / 4)]);
+  if (SPLIT > 1) {  // the CTA has one row: all its warps are here
+    part[warp][lane] = acc;
+    if (lane == 0) part_ml[warp] = make_float2(mm, ll);
+    __syncthreads();
+    if (warp > 0) return;
+    for (int k = 1; k < SPLIT; ++k) add(part_ml[k], part[k][lane]);
   }
-  const long long t = s.q0 + r / p.G;
-  const int h = g * p.G + r % p.G;
   const float inv = ll > 0.0f ? 1.0f / ll : (ll == 0.0f ? 0.0f : ll);
   *reinterpret_cast<uint2*>(P.out + t * P.out_stride + h * FA_HEAD_DIM + 4 * lane) =
       make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
@@ -651,6 +651,9 @@ static int rows_chunk(const fa_paged_shape& s, int tiles, int ctas) {
   const long long want = (ctas + units - 1) / units;
   long long c = (s.max_kv + want - 1) / want;
   c = (c + 63) / 64 * 64;
+  long long most = (s.max_kv + 47) / 48;  // at most 48 chunks a tile: they are merged
+  most = (most + 63) / 64 * 64;
+  if (c < most) c = most;
   return (int)(c < 256 ? 256 : c);
 }
 
@@ -687,8 +690,11 @@ static cudaError_t attend_plan(const fa_paged_shape& s, int window, AttendPlan* 
   P->slots = chunk_slots(s, window, P->chunk, (PR_ROWS + G - 1) / G);
   P->window = window;
   // Caches of at most 4096 tokens go in 8 chunks of at least 64 tokens that one cluster merges:
-  // the second kernel takes longer than such a chunk.
-  if (P->max_rows > 0 && s.max_kv <= PR_CLUSTER * 512 && P->slots > 1) {
+  // the second kernel takes longer than such a chunk (one token over 2048 keys: 12 us with it, 10
+  // without). Where that makes more CTAs than are resident, single CTAs pack better than clusters
+  // (8 x 8 tiles over 3000 keys: 21 us against 25).
+  if (P->max_rows > 0 && s.max_kv <= PR_CLUSTER * 512 && P->slots > 1 &&
+      (long long)s.B * s.Hkv * PR_CLUSTER <= 3LL * sms) {
     const int c = ((s.max_kv + PR_CLUSTER - 1) / PR_CLUSTER + 63) / 64 * 64;
     const int n = chunk_slots(s, window, c, (PR_ROWS + G - 1) / G);
     if (n <= PR_CLUSTER) {
@@ -763,6 +769,8 @@ cudaError_t launch_paged_attend(const fa_paged_shape& s, const fa_paged_cache& c
   J.out = P.out;
   J.out_stride = out_stride;
   J.lse = lse;
+  int sms = 148;
+  if ((e = device_sm_count(&sms)) != cudaSuccess) return e;
   auto join = [&](int chunk, int slots, int tile_rows, int max_rows, int min_rows, const float* o,
                   const float2* ml) {
     J.chunk = chunk;
@@ -772,8 +780,12 @@ cudaError_t launch_paged_attend(const fa_paged_shape& s, const fa_paged_cache& c
     J.min_rows = min_rows;
     J.part_o = o;
     J.part_ml = ml;
-    const long long rows = max_rows > 0 ? (long long)s.B * s.Hkv * max_rows : (long long)s.total_q * s.Hq;
-    return launch_overlapped(paged_join_kernel, dim3((unsigned)((rows + 7) / 8)), 256, 0, stream, J);
+    const long long most = (long long)(s.max_q < s.total_q ? s.max_q : s.total_q) * P.p.G;
+    J.rows = most < max_rows ? (int)most : max_rows;
+    const long long rows = max_rows > 0 ? (long long)s.B * s.Hkv * J.rows : (long long)s.total_q * s.Hq;
+    if (rows <= 4 * sms)
+      return launch_overlapped(paged_join_kernel<8>, dim3((unsigned)rows), 256, 0, stream, J);
+    return launch_overlapped(paged_join_kernel<1>, dim3((unsigned)((rows + 7) / 8)), 256, 0, stream, J);
   };
   if (P.slots > 1 && !P.cluster &&
       (e = join(P.chunk, P.slots, PR_ROWS, P.max_rows, 0, part_o, part_ml)) != cudaSuccess)

@@ -876,7 +876,7 @@ int key_box(const fa_paged_shape& s) {
 
 // Tiles are used where some sequence may have more rows than one 16-row tile and the heads of
 // a token fit a 128-row tile. Keys are split when the tiles of the batch leave SMs idle: into
-// chunks of equal length (multiples of a block, at least 4 blocks) that fill one wave.
+// chunks of equal length (multiples of a block, at least 2 blocks) that fill one wave.
 cudaError_t tile_plan(const fa_paged_shape& s, int window, TilePlan* t) {
   memset(t, 0, sizeof(*t));
   const int G = s.Hq / s.Hkv;
@@ -893,7 +893,7 @@ cudaError_t tile_plan(const fa_paged_shape& s, int window, TilePlan* t) {
   const long long want = units < sms ? sms / units : 1;
   long long c = (s.max_kv + want - 1) / want;
   c = (c + PT_KEYS - 1) / PT_KEYS * PT_KEYS;
-  t->chunk = (int)(c < 4 * PT_KEYS ? 4 * PT_KEYS : c);
+  t->chunk = (int)(c < 2 * PT_KEYS ? 2 * PT_KEYS : c);
   t->slots = chunk_slots(s, window, t->chunk, T);
   t->records = t->slots == 1 ? 0 : (size_t)s.total_q * s.Hq * t->slots;
   return cudaSuccess;
