@@ -73,6 +73,11 @@ int check_cache(const fa_paged_shape* shape, const fa_paged_cache* cache, bool b
   return FA_OK;
 }
 
+bool overlap(const void* a, size_t na, const void* b, size_t nb) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + nb && y < x + na;
+}
+
 // A [total_q][heads][128] bf16 tensor with a token stride.
 int check_rows(const void* p, int64_t stride, int heads, const char* name) {
   if (int r = check_ptr(p, name)) return r;
@@ -231,6 +236,7 @@ int fa_paged_attend(const fa_paged_shape* shape, const fa_paged_cache* cache, co
   if (s.B == 0 || s.total_q == 0) return FA_OK;
   if (int r = check_rows(q, q_stride, s.Hq, "q")) return r;
   if (int r = check_rows(out, out_stride, s.Hq, "out")) return r;
+  if (out == q) return fail(FA_ERR_INVALID, "out must not be q");
   if (lse)
     if (int r = check_ptr(lse, "lse", 4)) return r;
   size_t need = 0;
@@ -302,13 +308,15 @@ int fa_evict(const fa_paged_shape* shape, const fa_paged_cache* cache, const flo
     if (int r = check_ptr(weights, "weights", 4)) return r;
   if (int r = check_ptr(index, "index", 4)) return r;
   if (int r = check_ptr(dst_len, "dst_len", 4)) return r;
-  if (dst_len == cache->kv_len)
-    return fail(FA_ERR_INVALID, "dst_len must not be the source's kv_len");
+  if (overlap(dst_len, 4 * (size_t)s.B, cache->kv_len, 4 * (size_t)s.B))
+    return fail(FA_ERR_INVALID, "dst_len overlaps the source's kv_len");
   if (dst_weights) {
     if (int r = check_ptr(dst_weights, "dst_weights", 4)) return r;
     if (dst_weights_ld < keep)
       return fail(FA_ERR_INVALID, "dst_weights_ld=%lld is below keep=%d", (long long)dst_weights_ld, keep);
-    if (dst_weights == weights) return fail(FA_ERR_INVALID, "dst_weights must not be weights");
+    const size_t rows = (size_t)s.B * s.Hkv;
+    if (s.max_kv > 0 && overlap(dst_weights, 4 * rows * dst_weights_ld, weights, 4 * rows * weights_ld))
+      return fail(FA_ERR_INVALID, "dst_weights overlaps weights");
   }
   size_t need = 0;
   if (int r = launched(fa::evict_workspace(s, keep, &need), "fa_evict: configure")) return r;

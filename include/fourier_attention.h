@@ -460,8 +460,8 @@ int fa_rope(const fa_rope_plan* rope, int32_t B, int32_t T, int32_t H, const int
  *   positions  device int32 [total_q], or NULL: the cache index of each token. (A cache that
  *              fa_evict has cut has fewer tokens than positions: pass them then.)
  *   q, q_out   device bf16 [total_q][Hq][128] with token strides q_stride, q_out_stride (in
- *              elements), or both NULL. q_out = rotated q; q_out may be q (same stride).
- *              Without rope they must be NULL.
+ *              elements), or both NULL. q_out = rotated q; q_out may be q (same stride), any
+ *              other overlap is undefined. Without rope they must be NULL.
  *   k, v       device bf16 [total_q][Hkv][128] with token strides k_stride, v_stride.
  * Token strides are multiples of 8, at least heads * 128. Two sequences (or two slots of
  * one) must not share a page that is written. Launches one kernel.
@@ -479,7 +479,7 @@ int fa_paged_append(const fa_paged_shape* shape, const fa_paged_cache* cache,
  *            >= Hq * 128).
  *   scale    softmax scale, 0 (picks 1/sqrt(128)) or 1e-20 to 1e20.
  *   window   0: the token at cache index p sees keys j <= p; > 0: p - window < j <= p.
- *   out      device bf16 [total_q][Hq][128], token stride out_stride.
+ *   out      device bf16 [total_q][Hq][128], token stride out_stride; must not overlap q.
  *   lse      device fp32 [total_q][Hq] or NULL: log of the sum of exp(score), the scores
  *            scaled; natural logarithm. Rows that see no key get out = 0, lse = -infinity.
  * fp32 scores, maxima and sums; the weights are rounded to bf16 before the product with V
@@ -525,7 +525,8 @@ int fa_paged_weights(const fa_paged_shape* shape, const fa_paged_cache* cache, c
  *   dst_weights  device fp32 [B][Hkv][dst_weights_ld] or NULL: weights of the kept tokens.
  *   index    device int32 [B][Hkv][keep]: cache index of each kept token, ascending, -1 behind
  *            the last.
- *   dst_len  device int32 [B]: min(kv_len, keep); may be dst_cache->kv_len.
+ *   dst_len  device int32 [B]: min(kv_len, keep); may be dst_cache->kv_len, must not overlap
+ *            the source's kv_len. dst_weights must not overlap weights.
  * Destination slots and weights behind the kept tokens are left as they were.
  *   workspace  at least fa_evict_workspace_size(shape, keep) bytes (may be 0, then may be
  *            NULL); calls that may overlap need one each.

@@ -696,27 +696,49 @@ def test_bad_page_is_reported_and_spares_the_others(seqs, entry):
     expect_device_error("page_table")
 
 
-@pytest.mark.parametrize("what", ["kv_long", "kv_negative", "q_descends", "q_past_total", "q_many"])
-def test_bad_lengths_are_reported(what):
-    st = make([(2, 60), (3, 40), (1, 9)], 4, 2, 16, seed=32)
+@pytest.mark.parametrize("seqs", [[(2, 60), (3, 40), (1, 9)], [(70, 160), (60, 90), (90, 100)]],
+                         ids=["decode", "chunk"])
+@pytest.mark.parametrize("what", ["kv_long", "kv_negative", "q_descends", "q_past_total", "q_many", "q_negative"])
+def test_bad_lengths_are_reported(what, seqs):
+    st = make(seqs, 4, 2, 16, seed=32)
+    total, longest = st["total"], seqs[0][1]
     if what == "kv_long":
-        st["kv_len"][1] = 61
+        st["kv_len"][1] = longest + 1
     elif what == "kv_negative":
         st["kv_len"][1] = -1
     elif what == "q_descends":
-        st["q_start"][1] = 6
+        st["q_start"][1] = total
     elif what == "q_past_total":
-        st["q_start"][3] = 7
+        st["q_start"][3] = total + 1
+    elif what == "q_negative":
+        st["q_start"][1] = -3
     else:
         st["q_start"][1] = 0
-        st["q_start"][2] = 6
+        st["q_start"][2] = total
     attend(st)
     expect_device_error("q_start or kv_len")
-    k = torch.zeros(6, 2, D, dtype=BF, device="cuda")
+    k = torch.zeros(total, 2, D, dtype=BF, device="cuda")
     fa.fa_paged_append(st["batch"], k, k)
     expect_device_error("q_start or kv_len")
-    fa.fa_paged_weights(st["batch"], st["q"], torch.zeros(6, 4, device="cuda"), torch.zeros(3, 2, 60, device="cuda"))
+    fa.fa_paged_weights(st["batch"], st["q"], torch.zeros(total, 4, device="cuda"),
+                        torch.zeros(3, 2, longest, device="cuda"))
     expect_device_error("q_start or kv_len")
+
+
+def test_stream_argument():
+    """The calls run on the stream they are given, behind what is queued there."""
+    st = make([(1, 900), (60, 300)], 8, 2, 32, seed=40)
+    side = torch.cuda.Stream()
+    q = torch.zeros_like(st["q"])
+    out, lse = torch.empty_like(q), torch.empty(q.shape[:2], device="cuda")
+    ws = torch.empty(max(16, fa.fa_paged_attend_workspace_size(st["batch"])), dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(20_000_000)
+        q.copy_(st["q"])
+    fa.fa_paged_attend(st["batch"], q, out, ws, lse=lse, stream=side)
+    fa.fa_device_status(side)
+    check_attend(st, out, lse, reference(st))
 
 
 def test_c_calls_without_rows_do_nothing():

@@ -134,7 +134,7 @@ def append_args(shape=None, cache=None, **kw):
 
 
 def attend_args(shape=None, cache=None, **kw):
-    a = dict(q=P, qs=1024, scale=0.0, window=0, out=P, os=1024, lse=P, ws=P, bytes=1 << 40)
+    a = dict(q=P, qs=1024, scale=0.0, window=0, out=2 * P, os=1024, lse=P, ws=P, bytes=1 << 40)
     a.update(kw)
     return (shape if shape is not None else shape_of(), cache if cache is not None else cache_of(), a["q"], a["qs"],
             a["scale"], a["window"], a["out"], a["os"], a["lse"], a["ws"], a["bytes"], None)
@@ -148,7 +148,7 @@ def weights_args(shape=None, cache=None, **kw):
 
 
 def evict_args(shape=None, cache=None, **kw):
-    a = dict(w=P, ld=320, keep=100, sink=4, recent=10, ds=shape_of(max_kv=112, max_pages=7),
+    a = dict(w=P, ld=320, keep=100, sink=4, recent=10, ds=shape_of(max_kv=112, max_pages=7),  # weights: 2 x 2 x 320 floats at P
              dc=cache_of(K=2 * P, V=2 * P, q_start=None, kv_len=None), dw=P + 65536, dld=100, index=P, n=P + 64, ws=None,
              bytes=0)
     a.update(kw)
@@ -206,7 +206,8 @@ def test_bad_caches(name, kw):
     ("fa_evict", dict(ds=shape_of(B=1)), 1), ("fa_evict", dict(ds=shape_of(Hq=8, Hkv=4)), 1),
     ("fa_evict", dict(ds=shape_of(num_pages=0)), 1), ("fa_evict", dict(dc=cache_of(page_table=None)), 1),
     ("fa_evict", dict(dc=cache_of(V=P + 8)), 1), ("fa_evict", dict(dw=P), 1), ("fa_evict", dict(dld=99), 1),
-    ("fa_evict", dict(index=None), 1), ("fa_evict", dict(n=None), 1), ("fa_evict", dict(n=P), 1)], ids=str)
+    ("fa_evict", dict(index=None), 1), ("fa_evict", dict(n=None), 1), ("fa_evict", dict(n=P), 1), ("fa_evict", dict(n=P + 4), 1), ("fa_evict", dict(dw=P + 2400), 1),
+    ("fa_paged_attend", dict(out=P), 1)], ids=str)
 def test_argument_refusals(name, kw, code):
     refused(code, name, *CALLS[name](**kw))
 
