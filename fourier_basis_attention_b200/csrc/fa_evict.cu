@@ -11,10 +11,12 @@
 // two bits of the mantissa: weights fall into tens of bins, so that few lanes of a warp count
 // into the same one.
 // The move reads and writes each kept row once.
-//   Measured (B200): 131072 tokens of 8 KV heads to 16384, 140 MB, in 47 us (selection 25, move
-// 24 when each starts cold); 24 sequences of up to 8191 to 2001, 370 MB, in 78 us (16 and 59, the
-// move at 95% of the measured copy bandwidth in rows of 256 bytes). The selection is a chain of 3 digits of some 3 us: a count, a
-// cluster barrier, a read of 64 KB of histograms, a scan.
+//   Measured (B200): 131072 tokens of 8 KV heads to 16384, 140 MB, in 45 us (selection 18, move
+// 24 when each starts cold); 24 sequences of up to 8191 to 2001, 370 MB, in 78 us (15 and 59, the
+// move at 95% of the measured copy bandwidth in rows of 256 bytes). The selection is a chain of
+// steps: the weights' way in 4 us, three digits of 2 to 3 (a count, a barrier, a scan), the
+// indices 3. Summing the histograms of a cluster by adding nonzero counts to the CTA that owns a
+// bin took 6 us less than reading all 8 histograms in each.
 #include "fa_paged.cuh"
 
 namespace fa {
@@ -53,19 +55,19 @@ __device__ __forceinline__ uint32_t evict_key(float w, int j, int kv, int sink, 
   return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
-__device__ __forceinline__ int ld_cluster_s32(uint32_t addr) {
-  int v;
-  asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+__device__ __forceinline__ int2 ld_cluster_int2(uint32_t addr) {
+  int2 v;
+  asm volatile("ld.shared::cluster.v2.s32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr) : "memory");
   return v;
 }
-
-__device__ __forceinline__ int4 ld_cluster_int4(uint32_t addr) {
-  int4 v;
-  asm volatile("ld.shared::cluster.v4.s32 {%0,%1,%2,%3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "r"(addr)
-               : "memory");
-  return v;
+__device__ __forceinline__ void add_cluster(uint32_t addr, int v) {
+  asm volatile("red.relaxed.cluster.shared::cluster.add.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+__device__ __forceinline__ void cluster_arrive() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
 // One cluster of `size` CTAs a (sequence, KV head); CTA r has the tokens [r per, (r + 1) per).
@@ -73,10 +75,10 @@ __global__ void __launch_bounds__(EV_THREADS)
     evict_select_kernel(const __grid_constant__ EvictParams P, int size, int held) {
   allow_next_kernel();
   extern __shared__ __align__(16) uint32_t keys[];
-  // counts of a digit, and their sums over the cluster; one histogram a digit, so that no CTA
-  // waits for the others to have read it
-  __shared__ __align__(16) int hists[3][EV_BINS], sums[EV_BINS];
-  __shared__ int above[EV_WARPS], equal[EV_WARPS], mine[2];
+  // counts of a digit; their sums over the cluster, 1 / size of the bins in each CTA
+  __shared__ __align__(16) int hist[EV_BINS], sums[3][EV_BINS];
+  __shared__ int above[EV_WARPS], equal[EV_WARPS];
+  __shared__ __align__(8) int mine[2];
   __shared__ int found[2];  // digit; tokens still wanted among the keys that share the prefix
   const int rank = size > 1 ? (int)cluster_ctarank() : 0;
   const int g = blockIdx.x / size, b = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -94,25 +96,37 @@ __global__ void __launch_bounds__(EV_THREADS)
   const int first = min(rank * per, kv), n = min(per, kv - first);
   const int n_held = min(n, held);
   auto far_key = [&](int i) { return evict_key(w[first + i], first + i, kv, P.sink, P.recent); };
+  // keys [i, i + 4) of the CTA; those past n are 0
+  auto four = [&](int i, uint32_t (&k)[4]) {
+    if (i + 4 <= n_held) {
+      const uint4 q = *reinterpret_cast<const uint4*>(keys + i);
+      k[0] = q.x; k[1] = q.y; k[2] = q.z; k[3] = q.w;
+    } else {
+#pragma unroll
+      for (int u = 0; u < 4; ++u) k[u] = i + u >= n ? 0u : i + u < n_held ? keys[i + u] : far_key(i + u);
+    }
+  };
+  for (int i = tid; i < 3 * EV_BINS; i += EV_THREADS) sums[0][i] = 0;
+  static_assert(EV_BINS == 2 * EV_THREADS, "a thread owns two bins");
+  *reinterpret_cast<int2*>(hist + 2 * tid) = make_int2(0, 0);
+  __syncthreads();
+  if (size > 1) cluster_arrive();  // the sums are zero
   uint32_t prefix = 0;
   int want = m;
-  for (int i = tid; i < 3 * EV_BINS; i += EV_THREADS) hists[0][i] = 0;
-  __syncthreads();
 #pragma unroll 1
   for (int digit = 0; digit < 3; ++digit) {
     const int shift = digit == 0 ? 21 : digit == 1 ? 10 : 0;
     const uint32_t known = digit == 0 ? 0u : digit == 1 ? 0xFFE00000u : 0xFFFFFC00u;
     const uint32_t mask = digit == 2 ? 1023u : 2047u;
-    int* hist = hists[digit];
     if (digit == 0) {
-      // the weights come in once: 8 loads a thread on their way at a time
-      for (int i0 = tid; i0 < n_held; i0 += 8 * EV_THREADS) {
-        float x[8];
+      // the weights come in once: 16 loads a thread on their way at a time
+      for (int i0 = tid; i0 < n_held; i0 += 16 * EV_THREADS) {
+        float x[16];
 #pragma unroll
-        for (int u = 0; u < 8; ++u)
+        for (int u = 0; u < 16; ++u)
           if (i0 + u * EV_THREADS < n_held) x[u] = w[first + i0 + u * EV_THREADS];
 #pragma unroll
-        for (int u = 0; u < 8; ++u) {
+        for (int u = 0; u < 16; ++u) {
           const int i = i0 + u * EV_THREADS;
           if (i >= n_held) break;
           const uint32_t key = evict_key(x[u], first + i, kv, P.sink, P.recent);
@@ -120,44 +134,29 @@ __global__ void __launch_bounds__(EV_THREADS)
           atomicAdd(&hist[key >> 21], 1);
         }
       }
+      for (int i = n_held + tid; i < n; i += EV_THREADS) atomicAdd(&hist[far_key(i) >> 21], 1);
     } else {
-      for (int i = 4 * tid; i < n_held; i += 4 * EV_THREADS) {
-        const uint4 q = *reinterpret_cast<const uint4*>(keys + i);
-        const uint32_t k[4] = {q.x, q.y, q.z, q.w};
+      for (int i = 4 * tid; i < n; i += 4 * EV_THREADS) {
+        uint32_t k[4];
+        four(i, k);
 #pragma unroll
         for (int u = 0; u < 4; ++u)
-          if ((k[u] & known) == prefix && i + u < n_held) atomicAdd(&hist[(k[u] >> shift) & mask], 1);
-      }
-    }
-    for (int i = n_held + tid; i < n; i += EV_THREADS) {
-      const uint32_t key = far_key(i);
-      if ((key & known) == prefix) atomicAdd(&hist[(key >> shift) & mask], 1);
-    }
-    if (size > 1) {
-      cluster_sync_all();
-      if (tid < EV_BINS / 4) {
-        const uint32_t at = smem_u32(hist + 4 * tid);
-        int4 v[EV_CLUSTER];
-#pragma unroll
-        for (int r = 0; r < EV_CLUSTER; ++r)
-          if (r < size) v[r] = ld_cluster_int4(mapa_shared(at, r));
-        int4 t = v[0];
-#pragma unroll
-        for (int r = 1; r < EV_CLUSTER; ++r)
-          if (r < size) {
-            t.x += v[r].x;
-            t.y += v[r].y;
-            t.z += v[r].z;
-            t.w += v[r].w;
-          }
-        *reinterpret_cast<int4*>(sums + 4 * tid) = t;
+          if ((k[u] & known) == prefix && i + u < n) atomicAdd(&hist[(k[u] >> shift) & mask], 1);
       }
     }
     __syncthreads();
-    const int* total = size > 1 ? sums : hist;
-    // the digit at which the count from the top reaches `want`: 2 bins a thread
-    static_assert(EV_BINS == 2 * EV_THREADS, "bins a thread");
-    const int2 own = *reinterpret_cast<const int2*>(total + 2 * tid);
+    // this thread's two bins: their counts go to the CTA that sums them, and the sums come back
+    int2 own = *reinterpret_cast<const int2*>(hist + 2 * tid);
+    *reinterpret_cast<int2*>(hist + 2 * tid) = make_int2(0, 0);
+    if (size > 1) {
+      const uint32_t at = mapa_shared(smem_u32(&sums[digit][2 * tid]), (uint32_t)(2 * tid / (EV_BINS / size)));
+      if (digit == 0) cluster_wait();
+      if (own.x) add_cluster(at, own.x);
+      if (own.y) add_cluster(at + 4, own.y);
+      cluster_sync_all();
+      own = ld_cluster_int2(at);
+    }
+    // the digit at which the count from the top reaches `want`
     const int sum = own.x + own.y;
     int higher = sum;  // counts of this lane's bins and the warp's above
 #pragma unroll
@@ -168,8 +167,8 @@ __global__ void __launch_bounds__(EV_THREADS)
     if (lane == 0) above[warp] = higher;
     __syncthreads();
     higher -= sum;
-    higher += __reduce_add_sync(0xFFFFFFFFu, lane > warp ? above[lane] : 0);
     static_assert(EV_WARPS == 32, "a warp sums the warps' counts");
+    higher += __reduce_add_sync(0xFFFFFFFFu, lane > warp ? above[lane] : 0);
     if (higher < want && higher + own.y >= want) {
       found[0] = 2 * tid + 1;
       found[1] = want - higher;
@@ -183,21 +182,23 @@ __global__ void __launch_bounds__(EV_THREADS)
     prefix |= (uint32_t)found[0] << shift;
     want = found[1];
   }
-  // a warp's tokens [w0, w1): above the key, equal to it
-  const int seg = ((n + EV_WARPS - 1) / EV_WARPS + 31) & ~31;
+  // a warp's tokens [w0, w1), 4 a lane: above the key, equal to it (counts of 128 in 16 bits each)
+  const int seg = ((n + EV_WARPS - 1) / EV_WARPS + 127) & ~127;
   const int w0 = min(warp * seg, n), w1 = min(w0 + seg, n);
   int gt = 0, eq = 0;
-#pragma unroll 4
-  for (int i = w0 + lane; i < w1; i += 32) {
-    const uint32_t key = i < n_held ? keys[i] : far_key(i);
-    gt += key > prefix;
-    eq += key == prefix;
+  for (int i = w0 + 4 * lane; i < w1; i += 128) {
+    uint32_t k[4];
+    four(i, k);
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      gt += k[u] > prefix;
+      eq += k[u] == prefix && i + u < n;
+    }
   }
   gt = __reduce_add_sync(0xFFFFFFFFu, gt);
   eq = __reduce_add_sync(0xFFFFFFFFu, eq);
-  __syncthreads();  // `above` is read no more
   if (lane == 0) {
-    above[warp] = gt;
+    above[warp] = gt;  // every warp is past its last use: found was read after a barrier
     equal[warp] = eq;
   }
   __syncthreads();
@@ -213,27 +214,38 @@ __global__ void __launch_bounds__(EV_THREADS)
       }
     }
     cluster_sync_all();
-    int gt_r = 0, eq_r = 0;
-    if (lane < rank) {
-      gt_r = ld_cluster_s32(mapa_shared(smem_u32(&mine[0]), lane));
-      eq_r = ld_cluster_s32(mapa_shared(smem_u32(&mine[1]), lane));
+    int2 before = make_int2(0, 0);
+    if (lane < rank) before = ld_cluster_int2(mapa_shared(smem_u32(mine), lane));
+    gt_before += __reduce_add_sync(0xFFFFFFFFu, before.x);
+    eq_before += __reduce_add_sync(0xFFFFFFFFu, before.y);
+    cluster_arrive();  // reads no other CTA's shared memory any more
+  }
+  for (int i0 = w0; i0 < w1; i0 += 128) {
+    const int i = i0 + 4 * lane;
+    uint32_t k[4] = {0u, 0u, 0u, 0u};
+    if (i < w1) four(i, k);
+    int own = 0;
+#pragma unroll
+    for (int u = 0; u < 4; ++u) own += (k[u] > prefix ? 1 : 0) + (k[u] == prefix && i + u < w1 ? 1 << 16 : 0);
+    int upto = own;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int x = __shfl_up_sync(0xFFFFFFFFu, upto, d);
+      if (lane >= d) upto += x;
     }
-    gt_before += __reduce_add_sync(0xFFFFFFFFu, gt_r);
-    eq_before += __reduce_add_sync(0xFFFFFFFFu, eq_r);
-    cluster_sync_all();  // the CTA's shared memory is read no more
+    const int step = __shfl_sync(0xFFFFFFFFu, upto, 31);
+    int gi = gt_before + ((upto - own) & 0xFFFF), ei = eq_before + ((upto - own) >> 16);
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const bool is_gt = k[u] > prefix, is_eq = k[u] == prefix && i + u < w1;
+      if (is_gt || (is_eq && ei < want)) index[gi + min(ei, want)] = first + i + u;
+      gi += is_gt;
+      ei += is_eq;
+    }
+    gt_before += step & 0xFFFF;
+    eq_before += step >> 16;
   }
-  const unsigned below = (1u << lane) - 1u;
-  for (int i0 = w0; i0 < w1; i0 += 32) {
-    const int i = i0 + lane;
-    const uint32_t key = i >= w1 ? 0u : i < n_held ? keys[i] : far_key(i);
-    const bool is_gt = i < w1 && key > prefix, is_eq = i < w1 && key == prefix;
-    const unsigned bg = __ballot_sync(0xFFFFFFFFu, is_gt), be = __ballot_sync(0xFFFFFFFFu, is_eq);
-    const int e_rank = eq_before + __popc(be & below);
-    if (is_gt || (is_eq && e_rank < want))
-      index[gt_before + __popc(bg & below) + min(e_rank, want)] = first + i;
-    gt_before += __popc(bg);
-    eq_before += __popc(be);
-  }
+  if (size > 1) cluster_wait();  // nor does another CTA read this one's
 }
 
 // 16 lanes a row of 256 bytes; K and V of EM_ROWS kept tokens of one (sequence, KV head). A

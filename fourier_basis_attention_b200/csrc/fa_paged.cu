@@ -692,8 +692,11 @@ static cudaError_t attend_plan(const fa_paged_shape& s, int window, AttendPlan* 
   // Caches of at most 4096 tokens go in 8 chunks of at least 64 tokens that one cluster merges:
   // the second kernel takes longer than such a chunk (one token over 2048 keys: 12 us with it, 10
   // without). Where that makes more CTAs than are resident, single CTAs pack better than clusters
-  // (8 x 8 tiles over 3000 keys: 21 us against 25).
-  if (P->max_rows > 0 && s.max_kv <= PR_CLUSTER * 512 && P->slots > 1 &&
+  // (8 x 8 tiles over 3000 keys: 21 us against 25). Up to 512 tokens one CTA is as quick alone.
+  if (P->max_rows > 0 && s.max_kv <= 512) {
+    P->chunk = 512;
+    P->slots = 1;
+  } else if (P->max_rows > 0 && s.max_kv <= PR_CLUSTER * 512 && P->slots > 1 &&
       (long long)s.B * s.Hkv * PR_CLUSTER <= 3LL * sms) {
     const int c = ((s.max_kv + PR_CLUSTER - 1) / PR_CLUSTER + 63) / 64 * 64;
     const int n = chunk_slots(s, window, c, (PR_ROWS + G - 1) / G);
