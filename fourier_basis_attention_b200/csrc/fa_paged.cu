@@ -27,10 +27,10 @@ constexpr int PR_STAGE = 4 * PR_BOX;        // K and V, two boxes each
 constexpr int PW_STAGES = 3;
 constexpr int PW_STAGE = 2 * PR_BOX;        // K only
 constexpr int PR_OLD = FA_HEAD_DIM + 4;     // fp32 row of the merge buffer
+constexpr int PR_DEEP = 6;                  // stages of a launch that leaves SMs idle
+constexpr int PW_DEEP = 12;
 constexpr int PR_CLUSTER = 8;               // chunks that a cluster merges
 constexpr int PR_RING = PR_WARPS * PR_STAGES * PR_STAGE;
-constexpr int PR_SMEM = PR_RING + 1024;
-constexpr int PW_SMEM = PR_WARPS * PW_STAGES * PW_STAGE + 1024;
 static_assert(PR_WARPS * PR_ROWS * (PR_OLD + 2) * 4 + PR_ROWS * (FA_HEAD_DIM + 2) * 4 <= PR_RING,
               "merge buffers fit");
 
@@ -165,13 +165,15 @@ struct BlockRing {
   }
 };
 
-__global__ void __launch_bounds__(PR_THREADS, 3)
+// STAGES: blocks of a warp on their way, PR_STAGES with 3 CTAs an SM, or PR_DEEP with one.
+template <int STAGES>
+__global__ void __launch_bounds__(PR_THREADS, STAGES == PR_STAGES ? 3 : 1)
     paged_rows_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
                       const __grid_constant__ RowsParams P) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
-  __shared__ uint64_t full[PR_WARPS][PR_STAGES];
+  __shared__ uint64_t full[PR_WARPS][STAGES];
   __shared__ int abort_word;
   allow_next_kernel();
   const PagedBatch& p = P.p;
@@ -191,14 +193,14 @@ __global__ void __launch_bounds__(PR_THREADS, 3)
 
   if (threadIdx.x == 0) {
     abort_word = 0;
-    for (int i = 0; i < PR_WARPS * PR_STAGES; ++i) mbar_init(&full[0][0] + i, 1);
+    for (int i = 0; i < PR_WARPS * STAGES; ++i) mbar_init(&full[0][0] + i, 1);
     fence_barrier_init();
   }
   __syncthreads();
   volatile int* abort_flag = &abort_word;
 
-  BlockRing<PR_STAGES, PR_STAGE, true> ring;
-  ring.buf = smem + warp * PR_STAGES * PR_STAGE;
+  BlockRing<STAGES, PR_STAGE, true> ring;
+  ring.buf = smem + warp * STAGES * PR_STAGE;
   ring.full = full[warp];
   ring.tk = &tk;
   ring.tv = &tv;
@@ -208,8 +210,7 @@ __global__ void __launch_bounds__(PR_THREADS, 3)
   ring.k0 = k_lo + warp * PR_KEYS;
   const int left = k_hi - ring.k0;
   ring.n = left > 0 ? (left + PR_WARPS * PR_KEYS - 1) / (PR_WARPS * PR_KEYS) : 0;
-  if (lane == 0)
-    for (int i = 0; i < min(PR_STAGES, ring.n); ++i) ring.issue(i, ring.row_of(i));
+  if (lane < min(STAGES, ring.n)) ring.issue(lane, ring.row_of(lane));  // a block a lane
 
   uint32_t qf[8][4];
   load_q(P, s, g, r0, rows, lane, qf);
@@ -227,10 +228,10 @@ __global__ void __launch_bounds__(PR_THREADS, 3)
     for (int v = 0; v < 4; ++v) o[n][v] = 0.0f;
 
   for (int i = 0; i < ring.n; ++i) {
-    const int st = i % PR_STAGES;
+    const int st = i % STAGES;
     int next = 0;  // looked up while this block is on its way
-    if (lane == 0 && i + PR_STAGES < ring.n) next = ring.row_of(i + PR_STAGES);
-    const bool ok = mbar_wait(&ring.full[st], (uint32_t)(i / PR_STAGES) & 1u, abort_flag, WD_PAGED | 1u);
+    if (lane == 0 && i + STAGES < ring.n) next = ring.row_of(i + STAGES);
+    const bool ok = mbar_wait(&ring.full[st], (uint32_t)(i / STAGES) & 1u, abort_flag, WD_PAGED | 1u);
     if (!__all_sync(0xFFFFFFFFu, ok)) {
       if (lane == 0) ring.drain(i);
       break;
@@ -305,7 +306,7 @@ __global__ void __launch_bounds__(PR_THREADS, 3)
       mma_16816(o[n + 1], pf, v[2], v[3]);
     }
     __syncwarp();
-    if (lane == 0 && i + PR_STAGES < ring.n) ring.issue(i + PR_STAGES, next);
+    if (lane == 0 && i + STAGES < ring.n) ring.issue(i + STAGES, next);
   }
 #pragma unroll
   for (int u = 0; u < 2; ++u) {
@@ -494,13 +495,14 @@ __global__ void __launch_bounds__(256) paged_join_kernel(const __grid_constant__
 
 // Weights: a warp owns its blocks of 16 keys and runs over every tile of query rows that sees
 // them, so a key's sum is taken by one warp in one order.
-__global__ void __launch_bounds__(PR_THREADS, 4)
+template <int STAGES>
+__global__ void __launch_bounds__(PR_THREADS, STAGES == PW_STAGES ? 4 : 1)
     paged_weights_rows_kernel(const __grid_constant__ CUtensorMap tk,
                               const __grid_constant__ RowsParams P) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
-  __shared__ uint64_t full[PR_WARPS][PW_STAGES];
+  __shared__ uint64_t full[PR_WARPS][STAGES];
   __shared__ int abort_word;
   allow_next_kernel();
   const PagedBatch& p = P.p;
@@ -516,12 +518,12 @@ __global__ void __launch_bounds__(PR_THREADS, 4)
   if (k_lo >= k_hi) return;
   if (threadIdx.x == 0) {
     abort_word = 0;
-    for (int i = 0; i < PR_WARPS * PW_STAGES; ++i) mbar_init(&full[0][0] + i, 1);
+    for (int i = 0; i < PR_WARPS * STAGES; ++i) mbar_init(&full[0][0] + i, 1);
     fence_barrier_init();
   }
   __syncthreads();
-  BlockRing<PW_STAGES, PW_STAGE, false> ring;
-  ring.buf = smem + warp * PW_STAGES * PW_STAGE;
+  BlockRing<STAGES, PW_STAGE, false> ring;
+  ring.buf = smem + warp * STAGES * PW_STAGE;
   ring.full = full[warp];
   ring.tk = &tk;
   ring.tv = nullptr;
@@ -531,8 +533,7 @@ __global__ void __launch_bounds__(PR_THREADS, 4)
   ring.k0 = k_lo + warp * PR_KEYS;
   const int left = k_hi - ring.k0;
   ring.n = left > 0 ? (left + PR_WARPS * PR_KEYS - 1) / (PR_WARPS * PR_KEYS) : 0;
-  if (lane == 0)
-    for (int i = 0; i < min(PW_STAGES, ring.n); ++i) ring.issue(i, ring.row_of(i));
+  if (lane < min(STAGES, ring.n)) ring.issue(lane, ring.row_of(lane));  // a block a lane
 
   uint32_t qf[8][4];
   float ls[2];
@@ -547,12 +548,12 @@ __global__ void __launch_bounds__(PR_THREADS, 4)
   };
   float old = old_weight(0);
   for (int i = 0; i < ring.n; ++i) {
-    const int st = i % PW_STAGES;
+    const int st = i % STAGES;
     // the next loads that the block's end needs, a block ahead
     const float old_next = old_weight(i + 1);
     int next = 0;
-    if (lane == 0 && i + PW_STAGES < ring.n) next = ring.row_of(i + PW_STAGES);
-    const bool ok = mbar_wait(&ring.full[st], (uint32_t)(i / PW_STAGES) & 1u, &abort_word, WD_PAGED | 2u);
+    if (lane == 0 && i + STAGES < ring.n) next = ring.row_of(i + STAGES);
+    const bool ok = mbar_wait(&ring.full[st], (uint32_t)(i / STAGES) & 1u, &abort_word, WD_PAGED | 2u);
     if (!__all_sync(0xFFFFFFFFu, ok)) {
       if (lane == 0) ring.drain(i);
       break;
@@ -592,7 +593,7 @@ __global__ void __launch_bounds__(PR_THREADS, 4)
         }
     }
     __syncwarp();
-    if (lane == 0 && i + PW_STAGES < ring.n) ring.issue(i + PW_STAGES, next);
+    if (lane == 0 && i + STAGES < ring.n) ring.issue(i + STAGES, next);
     // sum over the 8 lanes of a key, halving what a lane holds at each exchange
     const bool n1 = lane & 16, odd = lane & 8;
     float a = n1 ? sum[2] : sum[0], c = n1 ? sum[3] : sum[1];
@@ -692,9 +693,9 @@ static cudaError_t attend_plan(const fa_paged_shape& s, int window, AttendPlan* 
   // Caches of at most 4096 tokens go in 8 chunks of at least 64 tokens that one cluster merges:
   // the second kernel takes longer than such a chunk (one token over 2048 keys: 12 us with it, 10
   // without). Where that makes more CTAs than are resident, single CTAs pack better than clusters
-  // (8 x 8 tiles over 3000 keys: 21 us against 25). Up to 512 tokens one CTA is as quick alone.
-  if (P->max_rows > 0 && s.max_kv <= 512) {
-    P->chunk = 512;
+  // (8 x 8 tiles over 3000 keys: 21 us against 25). Up to 256 tokens one CTA is quicker alone.
+  if (P->max_rows > 0 && s.max_kv <= 256) {
+    P->chunk = 256;
     P->slots = 1;
   } else if (P->max_rows > 0 && s.max_kv <= PR_CLUSTER * 512 && P->slots > 1 &&
       (long long)s.B * s.Hkv * PR_CLUSTER <= 3LL * sms) {
@@ -724,8 +725,9 @@ cudaError_t launch_paged_attend(const fa_paged_shape& s, const fa_paged_cache& c
                                 cudaStream_t stream, const char** why) {
   AttendPlan a;
   size_t bytes = 0;
-  cudaError_t e = attend_plan(s, window, &a, &bytes);
-  if (e != cudaSuccess) return e;
+  int sms = 148;
+  cudaError_t e = device_sm_count(&sms);
+  if (e != cudaSuccess || (e = attend_plan(s, window, &a, &bytes)) != cudaSuccess) return e;
   float* part_o = static_cast<float*>(workspace);
   float2* part_ml = reinterpret_cast<float2*>(part_o + (a.rows_records + a.t.records) * FA_HEAD_DIM);
   RowsParams& P = a.r;
@@ -743,13 +745,17 @@ cudaError_t launch_paged_attend(const fa_paged_shape& s, const fa_paged_cache& c
     *why = "cuTensorMapEncodeTiled rejected the pools";
     return cudaErrorInvalidValue;
   }
-  if ((e = raise_smem_limit(reinterpret_cast<const void*>(paged_rows_kernel), PR_SMEM)) != cudaSuccess)
-    return e;
+  // A launch that leaves SMs idle has the shared memory for all of a warp's blocks at once (on the
+  // device, one token over 256 keys: 8.0 us with 2 stages, 6.8 with 6; over 2048 keys 9.1 and 7.8).
+  const bool deep = (long long)P.slots * P.tiles * s.Hkv * s.B <= sms;
+  auto* kernel = deep ? paged_rows_kernel<PR_DEEP> : paged_rows_kernel<PR_STAGES>;
+  const int smem = PR_WARPS * (deep ? PR_DEEP : PR_STAGES) * PR_STAGE + 1024;
+  if ((e = raise_smem_limit(reinterpret_cast<const void*>(kernel), smem)) != cudaSuccess) return e;
   const dim3 grid((unsigned)(P.slots * P.tiles), (unsigned)s.Hkv, (unsigned)s.B);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(PR_THREADS, 1, 1);
-  cfg.dynamicSmemBytes = PR_SMEM;
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -758,7 +764,7 @@ cudaError_t launch_paged_attend(const fa_paged_shape& s, const fa_paged_cache& c
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if ((e = cudaLaunchKernelEx(&cfg, paged_rows_kernel, tk, tv, P)) != cudaSuccess) return e;
+  if ((e = cudaLaunchKernelEx(&cfg, kernel, tk, tv, P)) != cudaSuccess) return e;
   float* tile_o = part_o + a.rows_records * FA_HEAD_DIM;
   float2* tile_ml = part_ml + a.rows_records;
   if (a.t.tok > 0 &&
@@ -772,8 +778,6 @@ cudaError_t launch_paged_attend(const fa_paged_shape& s, const fa_paged_cache& c
   J.out = P.out;
   J.out_stride = out_stride;
   J.lse = lse;
-  int sms = 148;
-  if ((e = device_sm_count(&sms)) != cudaSuccess) return e;
   auto join = [&](int chunk, int slots, int tile_rows, int max_rows, int min_rows, const float* o,
                   const float2* ml) {
     J.chunk = chunk;
@@ -825,10 +829,12 @@ cudaError_t launch_paged_weights(const fa_paged_shape& s, const fa_paged_cache& 
     *why = "cuTensorMapEncodeTiled rejected the pool";
     return cudaErrorInvalidValue;
   }
-  const void* fn = reinterpret_cast<const void*>(paged_weights_rows_kernel);
-  if ((e = raise_smem_limit(fn, PW_SMEM)) != cudaSuccess) return e;
+  const bool deep = (long long)P.slots * s.Hkv * s.B <= sms;  // as in launch_paged_attend
+  auto* kernel = deep ? paged_weights_rows_kernel<PW_DEEP> : paged_weights_rows_kernel<PW_STAGES>;
+  const int smem = PR_WARPS * (deep ? PW_DEEP : PW_STAGES) * PW_STAGE + 1024;
+  if ((e = raise_smem_limit(reinterpret_cast<const void*>(kernel), smem)) != cudaSuccess) return e;
   const dim3 grid((unsigned)P.slots, (unsigned)s.Hkv, (unsigned)s.B);
-  paged_weights_rows_kernel<<<grid, PR_THREADS, PW_SMEM, stream>>>(tk, P);
+  kernel<<<grid, PR_THREADS, smem, stream>>>(tk, P);
   if ((e = cudaGetLastError()) != cudaSuccess || !tiles) return e;
   return launch_weight_tiles(s, c, q, q_stride, scale, window, lse, weights, weights_ld, PR_ROWS,
                              stream, why);
