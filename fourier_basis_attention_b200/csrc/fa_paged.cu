@@ -646,9 +646,16 @@ bool encode_pool(CUtensorMap* map, const void* pool, const fa_paged_shape& s, in
 // least 256 keys (below that the merge costs more than the chunk's own read). Real batches are
 // shorter and ragged, so the targets are many CTAs an SM: 64 sequences of up to 16384 tokens
 // decode in 452, 366, 345, 356 us for 2, 8, 32, 64 a SM (3 are resident); key weights of 32
-// sequences of up to 8192 take 68, 63, 63, 68 us for 8, 16, 32, 64 (4 are resident).
-static int rows_chunk(const fa_paged_shape& s, int tiles, int ctas) {
+// sequences of up to 8192 take 68, 63, 63, 68 us for 8, 16, 32, 64 (4 are resident). A batch that
+// one wave of the `resident` CTAs can read in chunks of at most 768 keys is cut to fill that wave:
+// a second, partly filled one costs as much as the first (2 sequences of 8000 keys, 8 KV heads: 19
+// us in chunks of 256, 15 in chunks of 320; 8 of 3000 25 and 20).
+static int rows_chunk(const fa_paged_shape& s, int tiles, int ctas, int resident) {
   const long long units = (long long)s.B * s.Hkv * tiles;
+  if (resident >= 2 * units) {
+    const long long n = resident / units, c = ((s.max_kv + n - 1) / n + 63) / 64 * 64;
+    if (c >= 256 && c <= 768 && c * 48 >= s.max_kv) return (int)c;
+  }
   const long long want = (ctas + units - 1) / units;
   long long c = (s.max_kv + want - 1) / want;
   c = (c + 63) / 64 * 64;
@@ -687,7 +694,7 @@ static cudaError_t attend_plan(const fa_paged_shape& s, int window, AttendPlan* 
   memset(P, 0, sizeof(*P));
   P->max_rows = a->t.tok > 0 || rows <= PR_ROWS ? PR_ROWS : 0;
   P->tiles = P->max_rows > 0 ? 1 : (int)((rows + PR_ROWS - 1) / PR_ROWS);
-  P->chunk = rows_chunk(s, P->tiles, 32 * sms);
+  P->chunk = rows_chunk(s, P->tiles, 32 * sms, 3 * sms);
   P->slots = chunk_slots(s, window, P->chunk, (PR_ROWS + G - 1) / G);
   P->window = window;
   // Caches of at most 4096 tokens go in 8 chunks of at least 64 tokens that one cluster merges:
@@ -822,7 +829,7 @@ cudaError_t launch_paged_weights(const fa_paged_shape& s, const fa_paged_cache& 
   const long long max_q = s.max_q < s.total_q ? s.max_q : s.total_q;
   const bool tiles = P.p.G <= 128 && max_q * P.p.G > PR_ROWS;
   P.max_rows = tiles ? PR_ROWS : 0;
-  P.chunk = rows_chunk(s, 1, 16 * sms);
+  P.chunk = rows_chunk(s, 1, 16 * sms, 4 * sms);
   P.slots = chunk_slots(s, window, P.chunk, tiles ? PR_ROWS : (int)max_q);
   CUtensorMap tk;
   if (!encode_pool(&tk, c.K, s, PR_KEYS)) {
