@@ -875,8 +875,11 @@ int key_box(const fa_paged_shape& s) {
 }
 
 // Tiles are used where some sequence may have more rows than one 16-row tile and the heads of
-// a token fit a 128-row tile. Keys are split when the tiles of the batch leave SMs idle: into
-// chunks of equal length (multiples of a block, at least 2 blocks) that fill one wave.
+// a token fit a 128-row tile. Keys (of the window, where there is one) are split when the tiles
+// of the batch leave SMs idle: into chunks of equal length, multiples of a block and at least 2,
+// that fill one wave. More waves do not pay: a CTA's start and end take as long as 4 blocks, and
+// the parts are written and read again (600 tokens over 4000 keys, 80 pairs of tiles: 66 us whole,
+// 76 in 3 chunks; 4096 over 16384: 829 and 913 in 2).
 cudaError_t tile_plan(const fa_paged_shape& s, int window, TilePlan* t) {
   memset(t, 0, sizeof(*t));
   const int G = s.Hq / s.Hkv;
@@ -891,7 +894,11 @@ cudaError_t tile_plan(const fa_paged_shape& s, int window, TilePlan* t) {
   t->tiles = s.total_q / T + s.B;
   const long long units = (long long)((s.total_q + T - 1) / T) * s.Hkv;
   const long long want = units < sms ? sms / units : 1;
-  long long c = (s.max_kv + want - 1) / want;
+  long long c = s.max_kv;
+  if (want > 1) {
+    if (window > 0 && (long long)window + T < c) c = (long long)window + T;
+    c = (c + want - 1) / want;
+  }
   c = (c + PT_KEYS - 1) / PT_KEYS * PT_KEYS;
   t->chunk = (int)(c < 2 * PT_KEYS ? 2 * PT_KEYS : c);
   t->slots = chunk_slots(s, window, t->chunk, T);
