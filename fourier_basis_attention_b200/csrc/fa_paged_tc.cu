@@ -559,11 +559,11 @@ __global__ void __launch_bounds__(PT_THREADS, 1)
   wait_earlier_kernel();  // the rows of short sequences: this kernel needs none of them
 }
 
-// Weights that keys gather: w_j += sum_rows exp2(c s_rj - log2 e lse_r). A CTA keeps 256 keys
-// (two tiles) and streams the query rows that see them in blocks of 128, as S^T = K Q^T: a
-// thread owns a key (a lane of tensor memory) and sums along half its columns, so that nothing
-// is reduced across threads but the two halves and a key's sum is taken in one order. Scores are
-// double-buffered: the tensor core writes one buffer while the other is summed.
+// Weights that keys gather: w_j += sum_rows exp2(c s_rj - log2 e lse_r). An item is 256 keys (two
+// tiles) of a KV head, against which the query rows that see them stream in blocks of 128, as
+// S^T = K Q^T: a thread owns a key (a lane of tensor memory) and sums along half its columns, so
+// that nothing is reduced across threads but the two halves and a key's sum is taken in one order.
+// Scores are double-buffered: the tensor core writes one buffer while the other is summed.
 //   -lse / scale joins the product as 16 more dims: the keys hold 1, 1, 1, 0, ..., a row its
 // value in three bf16 parts (exact to 2^-24 of it, as an fp32 product would be). Read from shared
 // memory by every thread for every column it took as many cycles as the exponentials.
@@ -581,39 +581,98 @@ constexpr int PV_SMEM = (2 + PV_STAGES) * PT_BLOCK + (1 + PV_STAGES) * PV_EXTRA 
 struct WeightParams {
   PagedBatch p;
   int window, tok, box, skip_rows;
+  int key_bits;  // log2 of the keys of an item: 8, or 7 (one tile) where that leaves SMs idle
   float scale_log2, inv_scale;
   const float* lse;
   float* weights;
   long long weights_ld;
 };
 
-__device__ __forceinline__ void sum_weight_tiles(const CUtensorMap& tq, const CUtensorMap& tk,
-                                                 const WeightParams& P) {
+// The items of a batch in order of sequence, keys and KV head: the first keys, which most rows
+// see, first. Only sequences of more than skip_rows rows have any, and CTA i of n takes items
+// i, 2n - 1 - i, 2n + i, ..., so that each gets early and late ones. With a CTA for every item that
+// the shape allows, 64 single tokens and a chunk of 512 over 4096 keys each took 168 us, 46 of them
+// in empty CTAs (now 122), and 32 heads of 6000 tokens 222 (now 181: the next item's keys load
+// while the last block is summed). Every warp finds the items by itself, 32 sequences at a time.
+struct WeightItems {
+  int round = 0, b0 = 0, base = 0;    // first sequence of the group, items before it
+  int b, g, q0, n, p0, j0, lo, hi;    // sequence, head, new tokens and their position, keys
+  int two, blk0, nb;                  // second tile used, blocks of P.tok tokens that see the keys
+
+  __device__ bool next(const WeightParams& P, int lane) {
+    const PagedBatch& p = P.p;
+    const int ctas = (int)gridDim.x;
+    const int index = round * ctas + (round & 1 ? ctas - 1 - (int)blockIdx.x : (int)blockIdx.x);
+    ++round;
+    for (; b0 < p.B; b0 += 32) {
+      SeqSpan s = {0, 0, 0};
+      int first = 0, count = 0;
+      if (b0 + lane < p.B) s = seq_span(p, b0 + lane);
+      if (s.n * p.G > P.skip_rows && s.kv > 0) {
+        if (P.window > 0) first = max(0, s.kv - s.n - P.window + 1);
+        count = (((s.kv - 1) >> P.key_bits) - (first >> P.key_bits) + 1) * p.Hkv;
+      }
+      int end = count;
+#pragma unroll
+      for (int d = 1; d < 32; d *= 2) {
+        const int below = __shfl_up_sync(0xFFFFFFFFu, end, d);
+        if (lane >= d) end += below;
+      }
+      const unsigned past = __ballot_sync(0xFFFFFFFFu, base + end > index);
+      if (past == 0u) {
+        base += __shfl_sync(0xFFFFFFFFu, end, 31);
+        continue;
+      }
+      const int l = __ffs(past) - 1;
+      const int k = index - base - __shfl_sync(0xFFFFFFFFu, end - count, l);
+      b = b0 + l;
+      q0 = __shfl_sync(0xFFFFFFFFu, s.q0, l);
+      n = __shfl_sync(0xFFFFFFFFu, s.n, l);
+      hi = __shfl_sync(0xFFFFFFFFu, s.kv, l);
+      lo = __shfl_sync(0xFFFFFFFFu, first, l);
+      p0 = hi - n;
+      g = k % p.Hkv;
+      j0 = ((lo >> P.key_bits) + k / p.Hkv) << P.key_bits;
+      two = P.key_bits > 7 && j0 + PT_TILE < hi;
+      const int i0 = max(0, j0 - p0);
+      const int i1 = P.window > 0 ? min(n, min(j0 + (1 << P.key_bits), hi) - 1 + P.window - p0) : n;
+      blk0 = i0 / P.tok;
+      nb = (i1 + P.tok - 1) / P.tok - blk0;
+      return true;
+    }
+    return false;
+  }
+};
+
+// Joins the PV_SOFT warps that sum; true if `flag` was set in any.
+__device__ __forceinline__ bool sums_meet(bool flag) {
+  uint32_t any;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.or.pred q, 1, 512, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(any)
+      : "r"((uint32_t)flag)
+      : "memory");
+  return any != 0;
+}
+
+__global__ void __launch_bounds__(PV_THREADS, 1)
+    paged_weights_tile_kernel(const __grid_constant__ CUtensorMap tq,
+                              const __grid_constant__ CUtensorMap tk,
+                              const __grid_constant__ WeightParams P) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
   uint8_t* ring = smem + 2 * PT_BLOCK;
   uint8_t* ones = ring + PV_STAGES * PT_BLOCK;  // the keys' extra dims
   uint8_t* extra = ones + PV_EXTRA;             // [stage] the rows'
-  __shared__ uint64_t full[PV_STAGES], empty[PV_STAGES], k_full, s_full[4], s_empty[4], drained;
-  __shared__ float half_sum[PV_KEYS];
+  __shared__ uint64_t full[PV_STAGES], empty[PV_STAGES], k_full, k_empty, s_full[4], s_empty[4], drained;
+  __shared__ float half_sum[2][PV_KEYS];
   __shared__ uint32_t tmem_ptr;
   __shared__ int abort_word;
   const PagedBatch& p = P.p;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int g = blockIdx.y, b = blockIdx.z;
-  const SeqSpan s = seq_span(p, b);
-  if (s.n * p.G <= P.skip_rows || s.kv <= 0) return;
-  const int p0 = s.kv - s.n;  // position of the first new token
-  const int hi = s.kv, lo = P.window > 0 ? max(0, p0 - P.window + 1) : 0;
-  const int j0 = (lo / PV_KEYS + (int)blockIdx.x) * PV_KEYS;
-  if (j0 >= hi) return;
-  const int two = j0 + PT_TILE < hi;
-  // tokens that see a key of the tiles, in blocks of P.tok
-  const int i0 = max(0, j0 - p0);
-  const int i1 = P.window > 0 ? min(s.n, min(j0 + PV_KEYS, hi) - 1 + P.window - p0) : s.n;
-  const int blk0 = i0 / P.tok, nb = (i1 + P.tok - 1) / P.tok - blk0;
-  if (nb <= 0) return;
+  allow_next_kernel();
 
   if (threadIdx.x == 0) {
     abort_word = 0;
@@ -622,6 +681,7 @@ __device__ __forceinline__ void sum_weight_tiles(const CUtensorMap& tq, const CU
       mbar_init(&empty[i], 1);
     }
     mbar_init(&k_full, 1);
+    mbar_init(&k_empty, 1);
     mbar_init(&drained, 1);
     for (int i = 0; i < 4; ++i) {
       mbar_init(&s_full[i], 1);
@@ -650,63 +710,80 @@ __device__ __forceinline__ void sum_weight_tiles(const CUtensorMap& tq, const CU
 
   if (warp >= PV_SOFT) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+    WeightItems w;
+    int it = 0, c = 0;  // items, blocks so far
+    bool ok = true;
     if (warp == PV_SOFT) {
       // ---------------------------------------------------------------- producer
-      bool ok = true;
-      int issued = 0;
-      for (int t = 0; t < 1 + two; ++t) {
-        const int row = key_row(p, b, g, j0 + t * PT_TILE, P.box, lo, hi, lane);
-        if (t == 0 && lane == 0) mbar_arrive_expect_tx(&k_full, PT_BLOCK * (1 + two));
-        __syncwarp();
-        load_keys(smem + t * PT_BLOCK, &tk, &k_full, P.box, row, lane);
-      }
-      for (int i = 0; i < nb && ok; ++i) {
-        const int st = i % PV_STAGES;
-        if (i >= PV_STAGES)
-          ok = mbar_wait(&empty[st], (uint32_t)(i / PV_STAGES - 1) & 1u, abort_flag, WD_PAGED | 9u);
+      int k_issued = 0;
+      for (; ok && w.next(P, lane); ++it) {
+        int row[2];
+        for (int t = 0; t < 2; ++t) row[t] = key_row(p, w.b, w.g, w.j0 + t * PT_TILE, P.box, w.lo, w.hi, lane);
+        if (it > 0) ok = mbar_wait(&k_empty, (uint32_t)(it - 1) & 1u, abort_flag, WD_PAGED | 14u);
         ok = __all_sync(0xFFFFFFFFu, ok);
         if (!ok) break;
-        if (lane == 0) {
-          mbar_arrive_expect_tx(&full[st], (uint32_t)(P.tok * p.G * 256));
-          for (int h = 0; h < 2; ++h)
-            tma_load_3d(ring + st * PT_BLOCK + h * PT_HALF, &tq, &full[st], 64 * h, g * p.G,
-                        s.q0 + (blk0 + i) * P.tok);
+        if (lane == 0) mbar_arrive_expect_tx(&k_full, PT_BLOCK * (1 + w.two));
+        __syncwarp();
+        load_keys(smem, &tk, &k_full, P.box, row[0], lane);
+        if (w.two) load_keys(smem + PT_BLOCK, &tk, &k_full, P.box, row[1], lane);
+        ++k_issued;
+        for (int i = 0; i < w.nb; ++i, ++c) {
+          const int st = c % PV_STAGES;
+          if (c >= PV_STAGES)
+            ok = mbar_wait(&empty[st], (uint32_t)(c / PV_STAGES - 1) & 1u, abort_flag, WD_PAGED | 9u);
+          ok = __all_sync(0xFFFFFFFFu, ok);
+          if (!ok) break;
+          if (lane == 0) {
+            mbar_arrive_expect_tx(&full[st], (uint32_t)(P.tok * p.G * 256));
+            for (int h = 0; h < 2; ++h)
+              tma_load_3d(ring + st * PT_BLOCK + h * PT_HALF, &tq, &full[st], 64 * h, w.g * p.G,
+                          w.q0 + (w.blk0 + i) * P.tok);
+          }
         }
-        ++issued;
       }
       if (!ok && lane == 0) {
-        drain_ring<PV_STAGES>(full, issued);
-        drain_ring<1>(&k_full, 1);
+        drain_ring<PV_STAGES>(full, c);
+        drain_ring<1>(&k_full, k_issued);
       }
     } else if (warp == PV_SOFT + 1) {
       // ---------------------------------------------------------------- MMA
       constexpr uint32_t id = idesc_bf16_f32(PT_TILE, PT_TILE, false);
       const uint32_t a_lo = desc_lo(smem_u32(smem), 16), b_lo = desc_lo(smem_u32(ring), 16);
       const uint32_t one_lo = desc_lo(smem_u32(ones), PV_EXTRA / 2), x_lo = desc_lo(smem_u32(extra), PV_EXTRA / 2);
-      bool ok = mbar_wait(&k_full, 0, abort_flag, WD_PAGED | 10u);
-      for (int i = 0; i < nb; ++i) {
-        const int st = i % PV_STAGES, u = i & 1;
-        ok = ok && mbar_wait(&full[st], (uint32_t)(i / PV_STAGES) & 1u, abort_flag, WD_PAGED | 11u);
-        for (int t = 0; t < 1 + two; ++t) {
-          if (i >= 2)
-            ok = ok && mbar_wait(&s_empty[2 * t + u], (uint32_t)(i / 2 - 1) & 1u, abort_flag, WD_PAGED | 12u);
-          ok = __all_sync(0xFFFFFFFFu, ok);
-          if (!ok) break;
-          tc_fence_after();
-          if (elect_one()) {
+      int used[2] = {0, 0};  // score buffers of each tile so far
+      for (; ok && w.next(P, lane); ++it) {
+        ok = mbar_wait(&k_full, (uint32_t)it & 1u, abort_flag, WD_PAGED | 10u);
+        for (int i = 0; i < w.nb; ++i, ++c) {
+          const int st = c % PV_STAGES;
+          ok = ok && mbar_wait(&full[st], (uint32_t)(c / PV_STAGES) & 1u, abort_flag, WD_PAGED | 11u);
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-              const uint32_t off = ((k >> 2) * PT_HALF + (k & 3) * 32) >> 4;
-              mma_ss(tmem + 128 * (2 * t + u), a_lo + t * (PT_BLOCK >> 4) + off,
-                     b_lo + st * (PT_BLOCK >> 4) + off, id, k > 0);
+          for (int t = 0; t < 2; ++t) {
+            if (t > w.two) break;
+            const int u = used[t] & 1;
+            if (used[t] >= 2)
+              ok = ok && mbar_wait(&s_empty[2 * t + u], (uint32_t)(used[t] / 2 - 1) & 1u, abort_flag, WD_PAGED | 12u);
+            ok = __all_sync(0xFFFFFFFFu, ok);
+            if (!ok) break;
+            ++used[t];
+            tc_fence_after();
+            if (elect_one()) {
+#pragma unroll
+              for (int k = 0; k < 8; ++k) {
+                const uint32_t off = ((k >> 2) * PT_HALF + (k & 3) * 32) >> 4;
+                mma_ss(tmem + 128 * (2 * t + u), a_lo + t * (PT_BLOCK >> 4) + off,
+                       b_lo + st * (PT_BLOCK >> 4) + off, id, k > 0);
+              }
+              mma_ss(tmem + 128 * (2 * t + u), one_lo, x_lo + st * (PV_EXTRA >> 4), id, true, PV_EXTRA_HI);
+              mma_commit(&s_full[2 * t + u]);
+              if (t == w.two) {
+                mma_commit(&empty[st]);
+                if (i + 1 == w.nb) mma_commit(&k_empty);
+              }
             }
-            mma_ss(tmem + 128 * (2 * t + u), one_lo, x_lo + st * (PV_EXTRA >> 4), id, true, PV_EXTRA_HI);
-            mma_commit(&s_full[2 * t + u]);
-            if (t == two) mma_commit(&empty[st]);
           }
+          __syncwarp();
+          if (!ok) break;
         }
-        __syncwarp();
-        if (!ok) break;
       }
       if (!ok && elect_one()) {
         mma_commit(&drained);
@@ -717,41 +794,43 @@ __device__ __forceinline__ void sum_weight_tiles(const CUtensorMap& tq, const CU
     } else if (warp == PV_SOFT + 2) {
       // ---------------------------------------------------------------- log-sum-exp of the rows,
       // loaded a block ahead
-      auto load = [&](int i, float (&e)[4]) {
+      for (; ok && w.next(P, lane); ++it) {
+        auto load = [&](int i, float (&e)[4]) {
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          const int row = lane + 32 * x, tok = (blk0 + i) * P.tok + row / p.G;
-          e[x] = -INFINITY;
-          if (i < nb && row < P.tok * p.G && tok < s.n)
-            e[x] = P.lse[(long long)(s.q0 + tok) * p.Hq + g * p.G + row % p.G];
+          for (int x = 0; x < 4; ++x) {
+            const int row = lane + 32 * x, tok = (w.blk0 + i) * P.tok + row / p.G;
+            e[x] = -INFINITY;
+            if (i < w.nb && row < P.tok * p.G && tok < w.n)
+              e[x] = P.lse[(long long)(w.q0 + tok) * p.Hq + w.g * p.G + row % p.G];
+          }
+        };
+        float next[4];
+        load(0, next);
+        for (int i = 0; i < w.nb; ++i, ++c) {
+          const int st = c % PV_STAGES;
+          uint4 e[4];
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            // columns without a row, and rows that see no key, add nothing
+            const float v = next[x] == -INFINITY ? -3e38f : -next[x] * P.inv_scale;
+            const __nv_bfloat16 a = __float2bfloat16_rn(v);
+            const float r = v - __bfloat162float(a);
+            const __nv_bfloat16 b = __float2bfloat16_rn(r);
+            e[x] = make_uint4(__bfloat16_as_ushort(a) | (uint32_t)__bfloat16_as_ushort(b) << 16,
+                              __bfloat16_as_ushort(__float2bfloat16_rn(r - __bfloat162float(b))), 0u, 0u);
+          }
+          load(i + 1, next);
+          if (c >= PV_STAGES)
+            ok = mbar_wait(&empty[st], (uint32_t)(c / PV_STAGES - 1) & 1u, abort_flag, WD_PAGED | 13u);
+          ok = __all_sync(0xFFFFFFFFu, ok);
+          if (!ok) break;
+#pragma unroll
+          for (int x = 0; x < 4; ++x)
+            reinterpret_cast<uint4*>(extra + st * PV_EXTRA)[lane + 32 * x] = e[x];
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&full[st]);
         }
-      };
-      float next[4];
-      load(0, next);
-      for (int i = 0; i < nb; ++i) {
-        const int st = i % PV_STAGES;
-        uint4 e[4];
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          // columns without a row, and rows that see no key, add nothing
-          const float v = next[x] == -INFINITY ? -3e38f : -next[x] * P.inv_scale;
-          const __nv_bfloat16 a = __float2bfloat16_rn(v);
-          const float r = v - __bfloat162float(a);
-          const __nv_bfloat16 b = __float2bfloat16_rn(r);
-          e[x] = make_uint4(__bfloat16_as_ushort(a) | (uint32_t)__bfloat16_as_ushort(b) << 16,
-                            __bfloat16_as_ushort(__float2bfloat16_rn(r - __bfloat162float(b))), 0u, 0u);
-        }
-        load(i + 1, next);
-        bool ok = true;
-        if (i >= PV_STAGES)
-          ok = mbar_wait(&empty[st], (uint32_t)(i / PV_STAGES - 1) & 1u, abort_flag, WD_PAGED | 13u);
-        if (!__all_sync(0xFFFFFFFFu, ok)) break;
-#pragma unroll
-        for (int x = 0; x < 4; ++x)
-          reinterpret_cast<uint4*>(extra + st * PV_EXTRA)[lane + 32 * x] = e[x];
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&full[st]);
       }
     }
   } else {
@@ -759,16 +838,19 @@ __device__ __forceinline__ void sum_weight_tiles(const CUtensorMap& tq, const CU
     // ------------------------------------------------------------------ sums: two threads a key,
     // each with 64 columns of a block
     const int t = warp >> 3, half = (warp >> 2) & 1, row = 32 * (warp & 3) + lane;
-    const int jt = j0 + t * PT_TILE, j = jt + row;
-    float total = 0.0f;
-    if (t <= two) {
-      const uint32_t ts = tmem + 256 * t + 64 * half + ((uint32_t)((warp & 3) * 32) << 16);
-      const uint64_t c2 = pack2(P.scale_log2, P.scale_log2);
+    const uint32_t ts = tmem + 256 * t + 64 * half + ((uint32_t)((warp & 3) * 32) << 16);
+    const uint64_t c2 = pack2(P.scale_log2, P.scale_log2);
+    WeightItems w;
+    int used = 0;  // score buffers so far
+    for (int it = 0; w.next(P, lane); ++it) {
+      const int jt = w.j0 + t * PT_TILE, j = jt + row;
+      bool ok = true;
       uint64_t sum[2] = {0ull, 0ull};
-      for (int i = 0; i < nb; ++i) {
-        const int u = i & 1;
-        const bool ok = mbar_wait(&s_full[2 * t + u], (uint32_t)(i / 2) & 1u, abort_flag, WD_PAGED | 15u);
-        if (!__all_sync(0xFFFFFFFFu, ok)) break;
+      for (int i = 0; t <= w.two && i < w.nb; ++i, ++used) {
+        const int u = used & 1;
+        ok = mbar_wait(&s_full[2 * t + u], (uint32_t)(used / 2) & 1u, abort_flag, WD_PAGED | 15u);
+        ok = __all_sync(0xFFFFFFFFu, ok);
+        if (!ok) break;
         tc_fence_after();
         uint32_t sr[2][32];
         tmem_ld_32x32b_x32(ts + 128 * u, sr[0]);
@@ -778,7 +860,7 @@ __device__ __forceinline__ void sum_weight_tiles(const CUtensorMap& tq, const CU
         __syncwarp();
         if (lane == 0) mbar_arrive(&s_empty[2 * t + u]);
         // columns [first, last) see the key: tokens from position j on, below j + window
-        const int tok0 = (blk0 + i) * P.tok, pb = p0 + tok0, left = s.n - tok0;
+        const int tok0 = (w.blk0 + i) * P.tok, pb = w.p0 + tok0, left = w.n - tok0;
         const bool edge = jt + PT_TILE - 1 > pb || left < P.tok ||
                           (P.window > 0 && pb + P.tok > jt + P.window);
         auto add = [&](auto plain) {
@@ -814,12 +896,12 @@ __device__ __forceinline__ void sum_weight_tiles(const CUtensorMap& tq, const CU
       }
       float a0, a1;
       unpack2(add2(sum[0], sum[1]), &a0, &a1);
-      total = a0 + a1;
+      float* other = &half_sum[it & 1][t * PT_TILE + row];  // the item after next writes it again
+      if (half) *other = a0 + a1;
+      if (sums_meet(!ok)) break;
+      if (!half && t <= w.two && j >= w.lo && j < w.hi)
+        P.weights[((long long)w.b * p.Hkv + w.g) * P.weights_ld + j] += a0 + a1 + *other;
     }
-    if (half) half_sum[t * PT_TILE + row] = total;
-    asm volatile("bar.sync 1, 512;" ::: "memory");
-    if (!half && !*abort_flag && j >= lo && j < hi)
-      P.weights[((long long)b * p.Hkv + g) * P.weights_ld + j] += total + half_sum[t * PT_TILE + row];
   }
   tc_fence_before();
   __syncthreads();
@@ -827,14 +909,6 @@ __device__ __forceinline__ void sum_weight_tiles(const CUtensorMap& tq, const CU
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
-}
-
-__global__ void __launch_bounds__(PV_THREADS, 1)
-    paged_weights_tile_kernel(const __grid_constant__ CUtensorMap tq,
-                              const __grid_constant__ CUtensorMap tk,
-                              const __grid_constant__ WeightParams P) {
-  allow_next_kernel();
-  sum_weight_tiles(tq, tk, P);
   wait_earlier_kernel();  // the keys of short sequences: this kernel needs none of them
 }
 
@@ -966,9 +1040,16 @@ cudaError_t launch_weight_tiles(const fa_paged_shape& s, const fa_paged_cache& c
   const void* fn = reinterpret_cast<const void*>(paged_weights_tile_kernel);
   cudaError_t e = prepare_kernel(fn, PV_SMEM, PV_THREADS, PV_REGS, why);
   if (e != cudaSuccess) return e;
+  int sms = 148;
+  if ((e = device_sm_count(&sms)) != cudaSuccess) return e;
   const int max_q = s.max_q < s.total_q ? s.max_q : s.total_q;
-  const dim3 grid((unsigned)chunk_slots(s, window, PV_KEYS, max_q), (unsigned)s.Hkv, (unsigned)s.B);
-  return launch_overlapped(paged_weights_tile_kernel, grid, PV_THREADS, PV_SMEM, stream, tq, tk, P);
+  const long long heads = (long long)s.Hkv * s.B;
+  // One tile an item where two leave half of the SMs idle: more CTAs read more queries from L2, but
+  // each works on half the keys (2000 tokens over 2000 keys, 8 KV heads: 88 us in 64 items, 71 in 128).
+  P.key_bits = 2 * heads * chunk_slots(s, window, PV_KEYS, max_q) <= sms ? 7 : 8;
+  const long long items = heads * chunk_slots(s, window, 1 << P.key_bits, max_q);
+  return launch_overlapped(paged_weights_tile_kernel, dim3((unsigned)(items < sms ? items : sms)), PV_THREADS,
+                           PV_SMEM, stream, tq, tk, P);
 }
 
 }  // namespace fa

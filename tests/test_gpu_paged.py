@@ -129,6 +129,8 @@ CASES = {
     "g128": ([(1, 60), (7, 200), (2, 1100)], 128, 1, 16, 0),
     "g200": ([(1, 100), (3, 40)], 200, 1, 16, 9),
     "many_chunks": ([(5 + i % 40, 60 + (91 * i) % 300) for i in range(70)], 4, 1, 16, 0),
+    "many_items": ([(9 + i % 30 if i % 3 else 1, 100 + (91 * i) % 600) for i in range(60)], 16, 4, 16, 0),
+    "many_items_window": ([(9 + i % 30 if i % 3 else 1, 100 + (91 * i) % 600) for i in range(60)], 16, 4, 32, 150),
     "decode_over_4096": ([(1, 9001), (2, 4200), (1, 5)], 8, 2, 64, 0),
     "decode_4096": ([(1, 4096), (1, 1), (2, 513), (0, 9)], 8, 2, 128, 0),
     "decode_4096_window": ([(1, 4096), (3, 700), (1, 1)], 4, 1, 64, 600),
