@@ -132,14 +132,19 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a_tmem, uint32_t b_l
 }
 
 // 2^y of a pair on the FMA units: y = n + f with n whole and f in [-1/2, 1/2] (adding and
-// subtracting 1.5 * 2^23 rounds), a polynomial for 2^f (the minimax one by the Remez exchange
-// for the relative error, 7.5e-8 at degree 5), n added to its exponent.
-// Arguments below -125 count as -125, minus infinity and NaN too.
-__device__ __forceinline__ void exp2_pair(uint64_t y, float* a, float* b) {
+// subtracting 1.5 * 2^23 rounds; 127 more leaves 2^n's exponent in the low bits), a polynomial for
+// 2^f (the minimax one by the Remez exchange for the relative error, 7.5e-8 at degree 5), times
+// 2^n. Arguments below -125 count as -125, minus infinity too; NaN stays NaN.
+__device__ __forceinline__ float max_or_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t exp2_pair(uint64_t y) {
   float y0, y1;
   unpack2(y, &y0, &y1);
-  y = pack2(fmaxf(y0, -125.0f), fmaxf(y1, -125.0f));
-  const uint64_t magic = pack2(12582912.0f, 12582912.0f);
+  y = pack2(max_or_nan(y0, -125.0f), max_or_nan(y1, -125.0f));
+  const uint64_t magic = pack2(12583039.0f, 12583039.0f);
   const uint64_t t = add2(y, magic);
   const uint64_t f = add2(y, fma2(t, pack2(-1.0f, -1.0f), magic));
   uint64_t p = fma2(f, pack2(1.327647245e-03f, 1.327647245e-03f), pack2(9.675540961e-03f, 9.675540961e-03f));
@@ -147,11 +152,9 @@ __device__ __forceinline__ void exp2_pair(uint64_t y, float* a, float* b) {
   p = fma2(f, p, pack2(2.402212024e-01f, 2.402212024e-01f));
   p = fma2(f, p, pack2(6.931469440e-01f, 6.931469440e-01f));
   p = fma2(f, p, pack2(1.000000119e+00f, 1.000000119e+00f));
-  float p0, p1, t0, t1;
-  unpack2(p, &p0, &p1);
+  float t0, t1;
   unpack2(t, &t0, &t1);
-  *a = __int_as_float(__float_as_int(p0) + (__float_as_int(t0) << 23));
-  *b = __int_as_float(__float_as_int(p1) + (__float_as_int(t1) << 23));
+  return mul2(p, pack2(__int_as_float(__float_as_int(t0) << 23), __int_as_float(__float_as_int(t1) << 23)));
 }
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float r;
@@ -868,15 +871,13 @@ __global__ void __launch_bounds__(PV_THREADS, 1)
           for (int e = 0; e < 32; ++e) {
             const uint32_t* q = &sr[e >> 4][2 * (e & 15)];
             const uint64_t y = mul2(pack2(__uint_as_float(q[0]), __uint_as_float(q[1])), c2);
-            float a0, a1;
             if (decltype(plain)::value && e % 4 == 3) {
-              exp2_pair(y, &a0, &a1);
+              sum[e & 1] = add2(sum[e & 1], exp2_pair(y));
             } else {
+              float a0, a1;
               unpack2(y, &a0, &a1);
-              a0 = exp2_approx(a0);
-              a1 = exp2_approx(a1);
+              sum[e & 1] = add2(sum[e & 1], pack2(exp2_approx(a0), exp2_approx(a1)));
             }
-            sum[e & 1] = add2(sum[e & 1], pack2(a0, a1));
           }
         };
         if (edge) {

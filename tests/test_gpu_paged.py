@@ -173,6 +173,20 @@ def test_weights(name):
     assert torch.equal(acc, first)  # no atomics
 
 
+@pytest.mark.parametrize("row", [64, 65, 70, 71, 127, 199])
+def test_weights_of_a_nan_query(row):
+    # one head a KV head: row = token, 256 rows in two blocks; the keys that it sees get NaN
+    st = make([(256, 1000)], 2, 2, 32, seed=row)
+    st["q"][row, 0] = float("nan")
+    _, lse = attend(st)
+    acc = torch.zeros(1, 2, 1000, device="cuda")
+    fa.fa_paged_weights(st["batch"], st["q"], lse, acc)
+    fa.fa_device_status()
+    seen = 1000 - 256 + row + 1
+    assert torch.isnan(acc[0, 0, :seen]).all()
+    assert torch.isfinite(acc[0, 0, seen:]).all() and torch.isfinite(acc[0, 1]).all()
+
+
 @pytest.mark.parametrize("seqs", [[(1, 900), (1, 3)], [(200, 600)]], ids=["decode", "chunk"])
 @pytest.mark.parametrize("scale", [0.011, 4.0])
 def test_attend_scale_and_large_scores(seqs, scale):
