@@ -804,7 +804,7 @@ cudaError_t launch_paged_attend(const fa_paged_shape& s, const fa_paged_cache& c
   if (P.slots > 1 && !P.cluster &&
       (e = join(P.chunk, P.slots, PR_ROWS, P.max_rows, 0, part_o, part_ml)) != cudaSuccess)
     return e;
-  if (a.t.slots > 1) e = join(a.t.chunk, a.t.slots, 2 * a.t.tok * P.p.G, 0, PR_ROWS, tile_o, tile_ml);
+  if (a.t.slots > 1) e = join(a.t.chunk, a.t.slots, a.t.pair * a.t.tok * P.p.G, 0, PR_ROWS, tile_o, tile_ml);
   return e;
 }
 

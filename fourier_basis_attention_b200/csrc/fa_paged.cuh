@@ -104,6 +104,7 @@ int chunk_slots(const fa_paged_shape& s, int window, int chunk, int tokens);
 // Tensor-core tiles of a batch (fa_paged_tc.cu); tok = 0: not used.
 struct TilePlan {
   int tok, box, tiles, chunk, slots;
+  int pair;  // 128-row tiles a CTA
   size_t records;  // partial results
 };
 cudaError_t tile_plan(const fa_paged_shape& s, int window, TilePlan* t);

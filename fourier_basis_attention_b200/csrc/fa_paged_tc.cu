@@ -1,17 +1,20 @@
 // fa_paged_tc.cu -- attention of new tokens over a paged cache on tcgen05, for sequences with
 // more query rows than one 16-row tile (a row = one token and one query head of a KV head).
 //
-// A CTA takes two tiles of 128 rows of one KV head and streams its keys and values in blocks
-// of 128 through a ring of TMA boxes. Per block and tile: S = Q K^T into tensor memory, one
+// An SM works on two tiles of 128 rows and streams the keys and values of their KV head in
+// blocks of 128 through a ring of TMA boxes. Per block and tile: S = Q K^T into tensor memory, one
 // thread a row turns S into weights P = exp2(c s - m) (running reference m, running sum l),
 // writes P back over S in bf16, and O += P V reads P from tensor memory. While one tile's
-// threads work on their weights the tensor core works on the other tile.
+// threads work on their weights the tensor core works on the other tile. The two are one CTA's,
+// which share each block, or two CTAs', of which one starts or ends while the other computes.
 //   The reference m follows the running maximum only when it falls behind by 2^8: the weights
-// stay below 256, which costs bf16 and fp32 nothing, and the product m -> O (a pass over O in
-// tensor memory) runs a few times a row instead of once a block.
+// stay below 256, which costs bf16 and fp32 nothing, and scaling O (a pass over it in tensor
+// memory) runs a few times a row instead of once a block.
 //
 // Bound: 4 * 128 flops a (row, key) on the tensor core, and one exp2 (16 a clock and SM): for
 // a 128 x 128 tile 1024 clocks each.
+//
+// The last kernel here sums the weights that keys gather on the same tiles.
 #include <math.h>
 #include <string.h>
 
@@ -25,23 +28,29 @@ constexpr int PT_KEYS = 128;                  // keys a block
 constexpr int PT_TILE = 128;                  // rows a tile
 constexpr int PT_HALF = 128 * 128;            // 64 dims x 128 rows
 constexpr int PT_BLOCK = 2 * PT_HALF;         // bytes of a block of K, V or Q rows
-constexpr int PT_STAGES = 5;
-constexpr int PT_SOFT = 8;                    // warps that turn scores into weights
-constexpr int PT_WARPS = PT_SOFT + 4;         // and producer, MMA, log-sum-exp and an idle one
-constexpr int PT_THREADS = PT_WARPS * 32;
 
-// What the warps of the attention kernel share besides the blocks (no static arrays: the blocks
-// start at the aligned beginning of shared memory).
-struct TileShared {
-  uint64_t full[PT_STAGES], empty[PT_STAGES], q_full, s_full[2], p_full[4], o_full[2], drained;
-  uint32_t tmem;
-  int abort;
+// An attention CTA of NT tiles: 4 warps a tile turn scores into weights; besides them a producer,
+// an MMA warp and two idle ones. A CTA of one tile takes half of the SM's shared and tensor memory
+// and registers.
+template <int NT>
+struct Tiles {
+  static constexpr int SOFT = 4 * NT, THREADS = (SOFT + 4) * 32;
+  static constexpr int STAGES = NT == 2 ? 5 : 2;  // of the ring of key and value blocks
+  // What the warps share besides the blocks (no static arrays: the blocks start at the aligned
+  // beginning of shared memory).
+  struct Shared {
+    uint64_t full[STAGES], empty[STAGES], q_full, s_full[NT], p_full[2 * NT], o_full[NT], drained;
+    uint32_t tmem;
+    int abort;
+  };
+  static constexpr int SMEM = (NT + STAGES) * PT_BLOCK + (int)sizeof(Shared);
+  // Registers after setmaxnreg, a thread: the two sums must not pass what the launch gives the
+  // block, or the raise waits for good (launches check it).
+  static constexpr int MORE = 208, LESS = NT == 2 ? 88 : 48;
+  static constexpr int REGS = SOFT * 32 * MORE + 4 * 32 * LESS;
 };
-constexpr int PT_SMEM = (2 + PT_STAGES) * PT_BLOCK + (int)sizeof(TileShared);
-static_assert(PT_SMEM <= 232448, "fits the SM");
-// Registers after setmaxnreg, a thread: the two sums must not pass what the launch gives the
-// block, or the raise waits for good (launches check it).
-constexpr int PT_REGS = PT_SOFT * 32 * 208 + 4 * 32 * 88;
+static_assert(Tiles<2>::SMEM <= 232448, "one CTA fits the SM");
+static_assert(2 * (Tiles<1>::SMEM + 1024) <= 233472, "two CTAs fit the SM");
 constexpr float PT_SLACK = 8.0f;              // log2 by which the maximum may pass m
 
 struct TileParams {
@@ -230,11 +239,13 @@ __device__ __forceinline__ void drain_ring(uint64_t* full, int issued) {
   }
 }
 
+template <int NT>
 __device__ __forceinline__ void attend_tiles(const CUtensorMap& tq, const CUtensorMap& tk,
                                              const CUtensorMap& tv, const TileParams& P) {
   extern __shared__ __align__(1024) uint8_t smem[];
-  uint8_t* ring = smem + 2 * PT_BLOCK;
-  TileShared& sh = *reinterpret_cast<TileShared*>(ring + PT_STAGES * PT_BLOCK);
+  constexpr int SOFT = Tiles<NT>::SOFT, STAGES = Tiles<NT>::STAGES;
+  uint8_t* ring = smem + NT * PT_BLOCK;
+  typename Tiles<NT>::Shared& sh = *reinterpret_cast<typename Tiles<NT>::Shared*>(ring + STAGES * PT_BLOCK);
   uint64_t *full = sh.full, *empty = sh.empty, *s_full = sh.s_full, *p_full = sh.p_full;
   if (smem_u32(smem) & 1023u) {  // the swizzle counts from 1024-byte boundaries
     flag_entry(WD_PAGED | 19u);
@@ -245,14 +256,14 @@ __device__ __forceinline__ void attend_tiles(const CUtensorMap& tq, const CUtens
   const int g = blockIdx.x % p.Hkv, rest = blockIdx.x / p.Hkv;
   const int slot = rest % P.slots;
   const int x = P.tiles - 1 - rest / P.slots;  // late tokens (the most keys) first
-  const int T = 2 * P.tok;
+  const int T = NT * P.tok;
   const int b = tile_sequence(p, x, T, lane);
   if (b < 0) return;
   const SeqSpan s = seq_span(p, b);
   const int t0 = (x - (s.q0 / T + b)) * T;  // first token of the tile in its sequence
   if (t0 < 0 || t0 >= s.n || s.n * p.G <= P.skip_rows) return;
   const int n_tok = min(T, s.n - t0), p0 = s.kv - s.n + t0;  // tokens, position of the first
-  const int two = n_tok > P.tok;
+  const int two = NT == 2 && n_tok > P.tok;
   const int hi = p0 + n_tok, lo = P.window > 0 ? max(0, p0 - P.window + 1) : 0;
   const bool single = P.slots == 1;
   const int c0 = (lo / P.chunk + slot) * P.chunk;
@@ -265,300 +276,312 @@ __device__ __forceinline__ void attend_tiles(const CUtensorMap& tq, const CUtens
 
   if (threadIdx.x == 0) {
     sh.abort = 0;
-    for (int i = 0; i < PT_STAGES; ++i) {
+    for (int i = 0; i < STAGES; ++i) {
       mbar_init(&full[i], 1);
       mbar_init(&empty[i], 1);
     }
     mbar_init(&sh.q_full, 1);
     mbar_init(&sh.drained, 1);
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < NT; ++i) {
       mbar_init(&s_full[i], 1);
       mbar_init(&sh.o_full[i], 1);
     }
-    for (int i = 0; i < 4; ++i) mbar_init(&p_full[i], 4);
+    for (int i = 0; i < 2 * NT; ++i) mbar_init(&p_full[i], 4);
     fence_barrier_init();
   }
-  if (warp == PT_SOFT + 1) {
-    tmem_alloc(&sh.tmem, 512);
+  if (warp == SOFT + 1) {
+    tmem_alloc(&sh.tmem, 256 * NT);
     tmem_relinquish();
     tc_fence_before();
   }
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = sh.tmem;  // S / P of tiles 0, 1 at columns 0, 128; O at 256, 384
+  const uint32_t tmem = sh.tmem;  // S / P of tile t at column 128 t, O at 128 (NT + t)
   volatile int* abort_flag = &sh.abort;
-  // 168 registers a thread at launch: 8 warps take 208, 4 keep 88 (the sum is the same)
-  if (warp >= PT_SOFT) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
-  if (warp == PT_SOFT) {
-    // ------------------------------------------------------------------ producer
-    int issued = 0;
-    if (nb > 0) {
-      const int q_bytes = P.tok * p.G * 128;  // of one 64-dim half of a tile
-      if (lane == 0) {
-        mbar_arrive_expect_tx(&sh.q_full, (uint32_t)(q_bytes * (two ? 4 : 2)));
-        for (int i = 0; i < (two ? 4 : 2); ++i)
-          tma_load_3d(smem + (i >> 1) * PT_BLOCK + (i & 1) * PT_HALF, &tq, &sh.q_full, 64 * (i & 1),
-                      g * p.G, s.q0 + t0 + (i >> 1) * P.tok);
-      }
-      bool ok = true;
-      int next = key_row(p, b, g, k_lo, P.box, lo, hi, lane);
-      for (int i = 0; i < nb && ok; ++i) {
-        const int row = next;  // looked up a block ahead: the page table answers in 0.5 us
-        if (i + 1 < nb) next = key_row(p, b, g, k_lo + (i + 1) * PT_KEYS, P.box, lo, hi, lane);
+  // NT = 2: 168 registers a thread at launch, 8 warps take 208, 4 keep 88; NT = 1: 128, 4 take 208,
+  // 4 keep 48 (the sums are the same)
+  if (warp >= SOFT) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Tiles<NT>::LESS));
+    if (warp == SOFT) {
+      // ------------------------------------------------------------------ producer
+      int issued = 0;
+      if (nb > 0) {
+        const int q_bytes = P.tok * p.G * 128;  // of one 64-dim half of a tile
+        if (lane == 0) {
+          mbar_arrive_expect_tx(&sh.q_full, (uint32_t)(q_bytes * (two ? 4 : 2)));
+          for (int i = 0; i < (two ? 4 : 2); ++i)
+            tma_load_3d(smem + (i >> 1) * PT_BLOCK + (i & 1) * PT_HALF, &tq, &sh.q_full, 64 * (i & 1),
+                        g * p.G, s.q0 + t0 + (i >> 1) * P.tok);
+        }
+        bool ok = true;
+        int next = key_row(p, b, g, k_lo, P.box, lo, hi, lane);
+        for (int i = 0; i < nb && ok; ++i) {
+          const int row = next;  // looked up a block ahead: the page table answers in 0.5 us
+          if (i + 1 < nb) next = key_row(p, b, g, k_lo + (i + 1) * PT_KEYS, P.box, lo, hi, lane);
 #pragma unroll
-        for (int v = 0; v < 2; ++v) {
-          const int st = issued % PT_STAGES;
-          if (issued >= PT_STAGES)
-            ok = mbar_wait(&empty[st], (uint32_t)(issued / PT_STAGES - 1) & 1u, abort_flag, WD_PAGED | 3u);
-          ok = __all_sync(0xFFFFFFFFu, ok);
-          if (!ok) break;
-          if (lane == 0) mbar_arrive_expect_tx(&full[st], PT_BLOCK);
-          __syncwarp();
-          load_keys(ring + st * PT_BLOCK, v ? &tv : &tk, &full[st], P.box, row, lane);
-          ++issued;
+          for (int v = 0; v < 2; ++v) {
+            const int st = issued % STAGES;
+            if (issued >= STAGES)
+              ok = mbar_wait(&empty[st], (uint32_t)(issued / STAGES - 1) & 1u, abort_flag, WD_PAGED | 3u);
+            ok = __all_sync(0xFFFFFFFFu, ok);
+            if (!ok) break;
+            if (lane == 0) mbar_arrive_expect_tx(&full[st], PT_BLOCK);
+            __syncwarp();
+            load_keys(ring + st * PT_BLOCK, v ? &tv : &tk, &full[st], P.box, row, lane);
+            ++issued;
+          }
+        }
+        if (!ok && lane == 0) {
+          drain_ring<STAGES>(full, issued);
+          drain_ring<1>(&sh.q_full, 1);
         }
       }
-      if (!ok && lane == 0) {
-        drain_ring<PT_STAGES>(full, issued);
-        drain_ring<1>(&sh.q_full, 1);
-      }
-    }
-  } else if (warp == PT_SOFT + 1) {
-    // ------------------------------------------------------------------ MMA: one warp for both
-    // tiles, so that their products run one after the other and not interleaved
-    constexpr uint32_t id_s = idesc_bf16_f32(PT_TILE, PT_KEYS, false);
-    constexpr uint32_t id_o = idesc_bf16_f32(PT_TILE, FA_HEAD_DIM, true);
-    const uint32_t q_lo = desc_lo(smem_u32(smem), 16), kb_lo = desc_lo(smem_u32(ring), 16);
-    const uint32_t v_lo = desc_lo(smem_u32(ring), PT_HALF);
-    auto scores = [&](int t, int st) {
-      const uint32_t qa = q_lo + t * (PT_BLOCK >> 4), kb = kb_lo + st * (PT_BLOCK >> 4);
+    } else if (warp == SOFT + 1) {
+      // ------------------------------------------------------------------ MMA: one warp for both
+      // tiles, so that their products run one after the other and not interleaved
+      constexpr uint32_t id_s = idesc_bf16_f32(PT_TILE, PT_KEYS, false);
+      constexpr uint32_t id_o = idesc_bf16_f32(PT_TILE, FA_HEAD_DIM, true);
+      const uint32_t q_lo = desc_lo(smem_u32(smem), 16), kb_lo = desc_lo(smem_u32(ring), 16);
+      const uint32_t v_lo = desc_lo(smem_u32(ring), PT_HALF);
+      auto scores = [&](int t, int st) {
+        const uint32_t qa = q_lo + t * (PT_BLOCK >> 4), kb = kb_lo + st * (PT_BLOCK >> 4);
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const uint32_t off = ((k >> 2) * PT_HALF + (k & 3) * 32) >> 4;
-        mma_ss(tmem + 128 * t, qa + off, kb + off, id_s, k > 0);
+        for (int k = 0; k < 8; ++k) {
+          const uint32_t off = ((k >> 2) * PT_HALF + (k & 3) * 32) >> 4;
+          mma_ss(tmem + 128 * t, qa + off, kb + off, id_s, k > 0);
+        }
+        mma_commit(&s_full[t]);
+      };
+      auto loaded = [&](int c) {  // use c of the ring
+        return mbar_wait(&full[c % STAGES], (uint32_t)(c / STAGES) & 1u, abort_flag, WD_PAGED | 5u);
+      };
+      bool ok = nb > 0 && mbar_wait(&sh.q_full, 0, abort_flag, WD_PAGED | 4u) && loaded(0);
+      if (__all_sync(0xFFFFFFFFu, ok) && elect_one()) {
+        if (a0 == 0 && e0 > 0) scores(0, 0);
+        if (NT == 2 && a1 == 0 && e1 > 0) scores(1, 0);
+        mma_commit(&empty[0]);
       }
-      mma_commit(&s_full[t]);
-    };
-    auto loaded = [&](int c) {  // use c of the ring
-      return mbar_wait(&full[c % PT_STAGES], (uint32_t)(c / PT_STAGES) & 1u, abort_flag, WD_PAGED | 5u);
-    };
-    bool ok = nb > 0 && mbar_wait(&sh.q_full, 0, abort_flag, WD_PAGED | 4u) && loaded(0);
-    if (__all_sync(0xFFFFFFFFu, ok) && elect_one()) {
-      if (a0 == 0 && e0 > 0) scores(0, 0);
-      if (a1 == 0 && e1 > 0) scores(1, 0);
-      mma_commit(&empty[0]);
-    }
-    for (int i = 0; i < nb; ++i) {
-      const int sv = (2 * i + 1) % PT_STAGES, sk = (2 * i + 2) % PT_STAGES;
-      const bool more = i + 1 < nb;
-      // a wait that finds its phase complete still takes some 100 clocks: these come while the
-      // tensor core has work
-      ok = ok && loaded(2 * i + 1) && (!more || loaded(2 * i + 2));
-      const int j0 = k_lo + i * PT_KEYS;
-      if (ok && (j0 < lo || j0 + PT_KEYS > hi)) {
-        // values of keys outside [lo, hi) may be anything, NaN too: they count as zero
-        hide_values(ring + sv * PT_BLOCK, lo - j0, hi - j0, lane);
-            fence_proxy_async_smem();
-      }
-      for (int t = 0; t < 2 && ok; ++t) {
-        const int a = t ? a1 : a0, e = t ? e1 : e0;
-        if (a <= i && i < e) {
-          // the weights of keys 0-63 and 64-127 of the block: the first product runs while the
-          // others are still computed
+      for (int i = 0; i < nb; ++i) {
+        const int sv = (2 * i + 1) % STAGES, sk = (2 * i + 2) % STAGES;
+        const bool more = i + 1 < nb;
+        // a wait that finds its phase complete still takes some 100 clocks: these come while the
+        // tensor core has work
+        ok = ok && loaded(2 * i + 1) && (NT == 1 || !more || loaded(2 * i + 2));
+        const int j0 = k_lo + i * PT_KEYS;
+        if (ok && (j0 < lo || j0 + PT_KEYS > hi)) {
+          // values of keys outside [lo, hi) may be anything, NaN too: they count as zero
+          hide_values(ring + sv * PT_BLOCK, lo - j0, hi - j0, lane);
+          fence_proxy_async_smem();
+        }
+        for (int t = 0; t < NT && ok; ++t) {
+          const int a = t ? a1 : a0, e = t ? e1 : e0;
+          if (a <= i && i < e) {
+            // the weights of keys 0-63 and 64-127 of the block: the first product runs while the
+            // others are still computed
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            ok = ok && mbar_wait(&p_full[2 * t + h], (uint32_t)(i - a) & 1u, abort_flag, WD_PAGED | 6u);
-            if (!__all_sync(0xFFFFFFFFu, ok)) {
-              ok = false;
-              break;
-            }
-            tc_fence_after();
-            if (elect_one()) {
+            for (int h = 0; h < 2; ++h) {
+              ok = ok && mbar_wait(&p_full[2 * t + h], (uint32_t)(i - a) & 1u, abort_flag, WD_PAGED | 6u);
+              if (!__all_sync(0xFFFFFFFFu, ok)) {
+                ok = false;
+                break;
+              }
+              tc_fence_after();
+              if (elect_one()) {
 #pragma unroll
-              for (int k = 4 * h; k < 4 * h + 4; ++k)
-                mma_ts(tmem + 256 + 128 * t, tmem + 128 * t + 8 * k, v_lo + (sv * PT_BLOCK + 2048 * k) / 16,
-                       id_o, i > a || k > 0);
-              if (h == 1) {
-                if (more && i + 1 < e) scores(t, sk);
-                if (i + 1 == e) mma_commit(&sh.o_full[t]);
+                for (int k = 4 * h; k < 4 * h + 4; ++k)
+                  mma_ts(tmem + 128 * (NT + t), tmem + 128 * t + 8 * k, v_lo + (sv * PT_BLOCK + 2048 * k) / 16,
+                         id_o, i > a || k > 0);
+                if (h == 1 && NT == 2) {
+                  if (more && i + 1 < e) scores(t, sk);
+                  if (i + 1 == e) mma_commit(&sh.o_full[t]);
+                }
               }
             }
+          } else if (NT == 2 && more && i + 1 == a && a < e) {
+            if (elect_one()) scores(t, sk);
           }
-        } else if (more && i + 1 == a && a < e) {
-          if (elect_one()) scores(t, sk);
+        }
+        if (NT == 1) {
+          // two stages: the next values may load once this product is done, the keys before them
+          // are waited for last
+          if (ok && elect_one()) {
+            mma_commit(&empty[sv]);
+            if (i + 1 == e0) mma_commit(&sh.o_full[0]);
+          }
+          ok = ok && (!more || loaded(2 * i + 2));
+        }
+        if (!__all_sync(0xFFFFFFFFu, ok)) {
+          ok = false;
+          break;
+        }
+        if (elect_one()) {
+          if (NT == 2) mma_commit(&empty[sv]);
+          if (NT == 1 && more && i + 1 >= a0 && i + 1 < e0) scores(0, sk);
+          if (more) mma_commit(&empty[sk]);
         }
       }
-      if (!__all_sync(0xFFFFFFFFu, ok)) {
-        ok = false;
-        break;
-      }
-      if (elect_one()) {
-        mma_commit(&empty[sv]);
-        if (more) mma_commit(&empty[sk]);
+      if (nb > 0 && !ok && elect_one()) {
+        // tensor memory is released only after every MMA of this CTA has completed
+        mma_commit(&sh.drained);
+        const unsigned long long w0 = globaltimer_ns();
+        while (!mbar_try_wait(&sh.drained, 0))
+          if (globaltimer_ns() - w0 > 200000000ull) break;
       }
     }
-    if (nb > 0 && !ok && elect_one()) {
-      // tensor memory is released only after every MMA of this CTA has completed
-      mma_commit(&sh.drained);
-      const unsigned long long w0 = globaltimer_ns();
-      while (!mbar_try_wait(&sh.drained, 0))
-        if (globaltimer_ns() - w0 > 200000000ull) break;
-    }
-  }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
-  if ((warp >> 2) <= two) {
-    // ------------------------------------------------------------------ softmax, one row a thread
-    const int t = warp >> 2, row = threadIdx.x & 127;
-    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-    const uint32_t ts = tmem + 128 * t + lanes, to = ts + 256;
-    const int tok = t * P.tok + row / p.G;
-    const bool valid = row < P.tok * p.G && tok < n_tok;
-    const int pos = valid ? p0 + tok : -1;
-    // positions of the warp's rows, blocks of the tile
-    const int pw_first = p0 + t * P.tok + (row & ~31) / p.G;
-    const int pw_last = p0 + min(t * P.tok + min((row | 31) / p.G, P.tok - 1), n_tok - 1);
-    const int a = t ? a1 : a0, e_ = t ? e1 : e0;
-    const float c = P.scale_log2;
-    float m = -INFINITY, l = 0.0f;
-    bool ok = true;
-    for (int i = a; i < e_; ++i) {
-      ok = mbar_wait(&s_full[t], (uint32_t)(i - a) & 1u, abort_flag, WD_PAGED | 7u);
-      ok = __all_sync(0xFFFFFFFFu, ok);
-      if (!ok) break;
-      tc_fence_after();
-      uint32_t sr[4][32];
-      const int j0 = k_lo + i * PT_KEYS;
-      tmem_ld_32x32b_x32(ts, sr[0]);
-      tmem_ld_32x32b_x32(ts + 32, sr[1]);
-      tmem_ld_wait_for(sr[0], sr[1]);
-      tmem_ld_32x32b_x32(ts + 64, sr[2]);
-      tmem_ld_32x32b_x32(ts + 96, sr[3]);
-      float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(Tiles<NT>::MORE));
+    if ((warp >> 2) <= two) {
+      // ------------------------------------------------------------------ softmax, one row a thread
+      const int t = warp >> 2, row = threadIdx.x & 127;
+      const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+      const uint32_t ts = tmem + 128 * t + lanes, to = ts + 128 * NT;
+      const int tok = t * P.tok + row / p.G;
+      const bool valid = row < P.tok * p.G && tok < n_tok;
+      const int pos = valid ? p0 + tok : -1;
+      // positions of the warp's rows, blocks of the tile
+      const int pw_first = p0 + t * P.tok + (row & ~31) / p.G;
+      const int pw_last = p0 + min(t * P.tok + min((row | 31) / p.G, P.tok - 1), n_tok - 1);
+      const int a = t ? a1 : a0, e_ = t ? e1 : e0;
+      const float c = P.scale_log2;
+      float m = -INFINITY, l = 0.0f;
+      bool ok = true;
+      for (int i = a; i < e_; ++i) {
+        ok = mbar_wait(&s_full[t], (uint32_t)(i - a) & 1u, abort_flag, WD_PAGED | 7u);
+        ok = __all_sync(0xFFFFFFFFu, ok);
+        if (!ok) break;
+        tc_fence_after();
+        uint32_t sr[4][32];
+        const int j0 = k_lo + i * PT_KEYS;
+        tmem_ld_32x32b_x32(ts, sr[0]);
+        tmem_ld_32x32b_x32(ts + 32, sr[1]);
+        tmem_ld_wait_for(sr[0], sr[1]);
+        tmem_ld_32x32b_x32(ts + 64, sr[2]);
+        tmem_ld_32x32b_x32(ts + 96, sr[3]);
+        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-      for (int v = 0; v < 4; ++v) {
-        if (v == 2) tmem_ld_wait_for(sr[2], sr[3]);
-        // chunks of 32 keys that some row of the warp does not see
-        const int j = j0 + 32 * v;
-        if (j + 31 > pw_first || (P.window > 0 && j <= pw_last - P.window)) {
-          const int up = pos - j, down = P.window > 0 ? up - P.window : -1;
+        for (int v = 0; v < 4; ++v) {
+          if (v == 2) tmem_ld_wait_for(sr[2], sr[3]);
+          // chunks of 32 keys that some row of the warp does not see
+          const int j = j0 + 32 * v;
+          if (j + 31 > pw_first || (P.window > 0 && j <= pw_last - P.window)) {
+            const int up = pos - j, down = P.window > 0 ? up - P.window : -1;
 #pragma unroll
-          for (int e = 0; e < 32; ++e)
-            if (e > up || e <= down) sr[v][e] = 0xFF800000u;
+            for (int e = 0; e < 32; ++e)
+              if (e > up || e <= down) sr[v][e] = 0xFF800000u;
+          }
+#pragma unroll
+          for (int e = 0; e < 32; e += 2)
+            mx[(e >> 1) & 3] = max3(mx[(e >> 1) & 3], __uint_as_float(sr[v][e]), __uint_as_float(sr[v][e + 1]));
         }
-#pragma unroll
-        for (int e = 0; e < 32; e += 2)
-          mx[(e >> 1) & 3] = max3(mx[(e >> 1) & 3], __uint_as_float(sr[v][e]), __uint_as_float(sr[v][e + 1]));
-      }
-      const float top = c * max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]);
-      if (i == a) {
-        m = top;
-      } else {
-        const bool behind = valid && top > m + PT_SLACK;
-        if (__any_sync(0xFFFFFFFFu, behind)) {
-          const float m_new = behind ? top : m;
-          const float f = behind ? exp2_approx(m - m_new) : 1.0f;
-          m = m_new;
-          l *= f;
+        const float top = c * max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]);
+        if (i == a) {
+          m = top;
+        } else {
+          const bool behind = valid && top > m + PT_SLACK;
+          if (__any_sync(0xFFFFFFFFu, behind)) {
+            const float m_new = behind ? top : m;
+            const float f = behind ? exp2_approx(m - m_new) : 1.0f;
+            m = m_new;
+            l *= f;
 #pragma unroll 1
-          for (int v = 0; v < 4; ++v) {
-            uint32_t o[32];
+            for (int v = 0; v < 4; ++v) {
+              uint32_t o[32];
+              tmem_ld_32x32b_x32(to + 32 * v, o);
+              tmem_ld_wait();
+#pragma unroll
+              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(f * __uint_as_float(o[e]));
+              tmem_st_32x32b_x32(to + 32 * v, o);
+            }
+          }
+        }
+        const float base = m == -INFINITY ? 0.0f : m;
+        const uint64_t c2 = pack2(c, c), b2 = pack2(-base, -base);
+        uint64_t sum[2] = {0ull, 0ull};
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          uint32_t w[32];
+#pragma unroll
+          for (int e = 0; e < 32; ++e) {
+            const uint32_t* q = &sr[2 * h + (e >> 4)][2 * (e & 15)];
+            const uint64_t y = fma2(pack2(__uint_as_float(q[0]), __uint_as_float(q[1])), c2, b2);
+            float y0, y1;
+            unpack2(y, &y0, &y1);
+            y0 = exp2_approx(y0);
+            y1 = exp2_approx(y1);
+            sum[e & 1] = add2(sum[e & 1], pack2(y0, y1));
+            w[e] = pack_bf16(y0, y1);
+          }
+          tmem_st_32x32b_x32(ts + 32 * h, w);
+          tmem_st_wait();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&p_full[2 * t + h]);
+        }
+        float l0, l1;
+        unpack2(add2(sum[0], sum[1]), &l0, &l1);
+        l += l0 + l1;
+      }
+      if (e_ > a && ok) {
+        ok = mbar_wait(&sh.o_full[t], 0, abort_flag, WD_PAGED | 8u);
+        ok = __all_sync(0xFFFFFFFFu, ok);
+        tc_fence_after();
+      }
+      if (ok) {
+        const long long token = s.q0 + t0 + tok;
+        const int h = g * p.G + row % p.G;
+        const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);
+        const long long rec = (token * p.Hq + h) * P.slots + slot;
+#pragma unroll 1
+        for (int v = 0; v < 4; ++v) {
+          uint32_t o[32];
+          if (e_ > a) {
             tmem_ld_32x32b_x32(to + 32 * v, o);
             tmem_ld_wait();
+          } else {
 #pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(f * __uint_as_float(o[e]));
-            tmem_st_32x32b_x32(to + 32 * v, o);
+            for (int e = 0; e < 32; ++e) o[e] = 0u;
+          }
+          if (!valid) continue;
+          const int d = 32 * v;
+          if (single) {
+            uint4* dst = reinterpret_cast<uint4*>(P.out + token * P.out_stride + h * FA_HEAD_DIM + d);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              uint32_t w[4];
+#pragma unroll
+              for (int u = 0; u < 4; ++u)
+                w[u] = pack_bf16(inv * __uint_as_float(o[8 * e + 2 * u]),
+                                 inv * __uint_as_float(o[8 * e + 2 * u + 1]));
+              dst[e] = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+          } else {
+            uint4* dst = reinterpret_cast<uint4*>(P.part_o + rec * FA_HEAD_DIM + d);
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              dst[e] = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
           }
         }
-      }
-      const float base = m == -INFINITY ? 0.0f : m;
-      const uint64_t c2 = pack2(c, c), b2 = pack2(-base, -base);
-      uint64_t sum[2] = {0ull, 0ull};
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        uint32_t w[32];
-#pragma unroll
-        for (int e = 0; e < 32; ++e) {
-          const uint32_t* q = &sr[2 * h + (e >> 4)][2 * (e & 15)];
-          const uint64_t y = fma2(pack2(__uint_as_float(q[0]), __uint_as_float(q[1])), c2, b2);
-          float y0, y1;
-          unpack2(y, &y0, &y1);
-          y0 = exp2_approx(y0);
-          y1 = exp2_approx(y1);
-          sum[e & 1] = add2(sum[e & 1], pack2(y0, y1));
-          w[e] = pack_bf16(y0, y1);
-        }
-        tmem_st_32x32b_x32(ts + 32 * h, w);
-        tmem_st_wait();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&p_full[2 * t + h]);
-      }
-      float l0, l1;
-      unpack2(add2(sum[0], sum[1]), &l0, &l1);
-      l += l0 + l1;
-    }
-    if (e_ > a && ok) {
-      ok = mbar_wait(&sh.o_full[t], 0, abort_flag, WD_PAGED | 8u);
-      ok = __all_sync(0xFFFFFFFFu, ok);
-      tc_fence_after();
-    }
-    if (ok) {
-      const long long token = s.q0 + t0 + tok;
-      const int h = g * p.G + row % p.G;
-      const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);
-      const long long rec = (token * p.Hq + h) * P.slots + slot;
-#pragma unroll 1
-      for (int v = 0; v < 4; ++v) {
-        uint32_t o[32];
-        if (e_ > a) {
-          tmem_ld_32x32b_x32(to + 32 * v, o);
-          tmem_ld_wait();
-        } else {
-#pragma unroll
-          for (int e = 0; e < 32; ++e) o[e] = 0u;
-        }
-        if (!valid) continue;
-        const int d = 32 * v;
-        if (single) {
-          uint4* dst = reinterpret_cast<uint4*>(P.out + token * P.out_stride + h * FA_HEAD_DIM + d);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            uint32_t w[4];
-#pragma unroll
-            for (int u = 0; u < 4; ++u)
-              w[u] = pack_bf16(inv * __uint_as_float(o[8 * e + 2 * u]),
-                               inv * __uint_as_float(o[8 * e + 2 * u + 1]));
-            dst[e] = make_uint4(w[0], w[1], w[2], w[3]);
-          }
-        } else {
-          uint4* dst = reinterpret_cast<uint4*>(P.part_o + rec * FA_HEAD_DIM + d);
-#pragma unroll
-          for (int e = 0; e < 8; ++e)
-            dst[e] = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+        if (valid) {
+          if (!single) P.part_ml[rec] = make_float2(m, l);
+          else if (P.lse) P.lse[token * p.Hq + h] = 0.693147180559945309f * (m + log2f(l));
         }
       }
-      if (valid) {
-        if (!single) P.part_ml[rec] = make_float2(m, l);
-        else if (P.lse) P.lse[token * p.Hq + h] = 0.693147180559945309f * (m + log2f(l));
-      }
     }
-  }
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == PT_SOFT + 1) {
+  if (warp == SOFT + 1) {
     tc_fence_after();
-    tmem_dealloc(tmem, 512);
+    tmem_dealloc(tmem, 256 * NT);
   }
 }
 
-__global__ void __launch_bounds__(PT_THREADS, 1)
+template <int NT>
+__global__ void __launch_bounds__(Tiles<NT>::THREADS, 3 - NT)
     paged_tile_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
                       const __grid_constant__ CUtensorMap tv, const __grid_constant__ TileParams P) {
   allow_next_kernel();
-  attend_tiles(tq, tk, tv, P);
+  attend_tiles<NT>(tq, tk, tv, P);
   wait_earlier_kernel();  // the rows of short sequences: this kernel needs none of them
 }
 
@@ -950,11 +973,15 @@ int key_box(const fa_paged_shape& s) {
 }
 
 // Tiles are used where some sequence may have more rows than one 16-row tile and the heads of
-// a token fit a 128-row tile. Keys (of the window, where there is one) are split when the tiles
-// of the batch leave SMs idle: into chunks of equal length, multiples of a block and at least 2,
-// that fill one wave. More waves do not pay: a CTA's start and end take as long as 4 blocks, and
-// the parts are written and read again (600 tokens over 4000 keys, 80 pairs of tiles: 66 us whole,
-// 76 in 3 chunks; 4096 over 16384: 829 and 913 in 2).
+// a token fit a 128-row tile. CTAs of one tile, two an SM, where a tile sees at most 10 blocks, of
+// which its start and end would take 4, or no sequence fills more than one (6 chunks with a window
+// of 1024: 97 us with two tiles a CTA, 90 with one; 1000 tokens over themselves 26 and 24; 64 x 30
+// over 4000 keys 150 and 131); else CTAs of two, which read each block once (4 x 300 over 2000 keys
+// 41 and 45; 4096 over 16384 818 and 938).
+//   Keys (of the window, where there is one) are split when the tiles of the batch leave SMs idle:
+// into chunks of equal length, multiples of a block and at least 2, that fill one wave. More waves
+// do not pay: the parts are written and read again (600 tokens over 4000 keys, 80 pairs of tiles:
+// 66 us whole, 76 in 3 chunks; 4096 over 16384: 829 and 913 in 2).
 cudaError_t tile_plan(const fa_paged_shape& s, int window, TilePlan* t) {
   memset(t, 0, sizeof(*t));
   const int G = s.Hq / s.Hkv;
@@ -965,15 +992,14 @@ cudaError_t tile_plan(const fa_paged_shape& s, int window, TilePlan* t) {
   if (e != cudaSuccess) return e;
   t->tok = PT_TILE / G;
   t->box = key_box(s);
-  const int T = 2 * t->tok;
+  long long keys = s.max_kv;  // that a tile may see
+  if (window > 0 && (long long)window + t->tok < keys) keys = (long long)window + t->tok;
+  t->pair = keys <= 1280 || max_q <= t->tok ? 1 : 2;
+  const int T = t->pair * t->tok;
   t->tiles = s.total_q / T + s.B;
-  const long long units = (long long)((s.total_q + T - 1) / T) * s.Hkv;
-  const long long want = units < sms ? sms / units : 1;
-  long long c = s.max_kv;
-  if (want > 1) {
-    if (window > 0 && (long long)window + T < c) c = (long long)window + T;
-    c = (c + want - 1) / want;
-  }
+  const long long units = (long long)((s.total_q + T - 1) / T) * s.Hkv, ctas = (3 - t->pair) * sms;
+  const long long want = units < ctas ? ctas / units : 1;
+  long long c = want > 1 ? (keys + want - 1) / want : s.max_kv;
   c = (c + PT_KEYS - 1) / PT_KEYS * PT_KEYS;
   t->chunk = (int)(c < 2 * PT_KEYS ? 2 * PT_KEYS : c);
   t->slots = chunk_slots(s, window, t->chunk, T);
@@ -1010,11 +1036,15 @@ cudaError_t launch_tiles(const fa_paged_shape& s, const fa_paged_cache& c, const
     *why = "cuTensorMapEncodeTiled rejected q";
     return cudaErrorInvalidValue;
   }
-  const void* fn = reinterpret_cast<const void*>(paged_tile_kernel);
-  cudaError_t e = prepare_kernel(fn, PT_SMEM, PT_THREADS, PT_REGS, why);
-  if (e != cudaSuccess) return e;
-  const long long ctas = (long long)t.tiles * t.slots * s.Hkv;
-  return launch_overlapped(paged_tile_kernel, dim3((unsigned)ctas), PT_THREADS, PT_SMEM, stream, tq, tk, tv, P);
+  auto launch = [&](auto kernel, auto tiles) {
+    using Config = decltype(tiles);
+    const cudaError_t e = prepare_kernel(reinterpret_cast<const void*>(kernel), Config::SMEM, Config::THREADS,
+                                         Config::REGS, why);
+    if (e != cudaSuccess) return e;
+    const long long ctas = (long long)t.tiles * t.slots * s.Hkv;
+    return launch_overlapped(kernel, dim3((unsigned)ctas), Config::THREADS, Config::SMEM, stream, tq, tk, tv, P);
+  };
+  return t.pair == 2 ? launch(paged_tile_kernel<2>, Tiles<2>()) : launch(paged_tile_kernel<1>, Tiles<1>());
 }
 
 cudaError_t launch_weight_tiles(const fa_paged_shape& s, const fa_paged_cache& c, const void* q,

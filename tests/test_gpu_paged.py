@@ -131,6 +131,14 @@ CASES = {
     "many_chunks": ([(5 + i % 40, 60 + (91 * i) % 300) for i in range(70)], 4, 1, 16, 0),
     "many_items": ([(9 + i % 30 if i % 3 else 1, 100 + (91 * i) % 600) for i in range(60)], 16, 4, 16, 0),
     "many_items_window": ([(9 + i % 30 if i % 3 else 1, 100 + (91 * i) % 600) for i in range(60)], 16, 4, 32, 150),
+    # more than 1280 keys: two tiles a CTA
+    "pair_prompt": ([(1400, 1400)], 4, 1, 128, 0),
+    "pair_window": ([(300, 3001), (1, 2100), (257, 1300)], 8, 2, 64, 1300),
+    "pair_g3": ([(200, 2000), (90, 90), (1, 1400), (43, 1290)], 6, 2, 16, 0),
+    "pair_no_sharing": ([(300, 1500), (129, 129)], 4, 4, 80, 0),
+    "pair_not_cached": ([(300, 100), (150, 2000), (20, 10), (70, 0)], 8, 2, 16, 0),
+    "pair_many": ([(33 + i % 50, 300 + (211 * i) % 1200) for i in range(45)], 8, 2, 16, 0),
+    "one_tile_long": ([(30, 2500), (32, 4000), (5, 1300)], 8, 2, 32, 0),
     "decode_over_4096": ([(1, 9001), (2, 4200), (1, 5)], 8, 2, 64, 0),
     "decode_4096": ([(1, 4096), (1, 1), (2, 513), (0, 9)], 8, 2, 128, 0),
     "decode_4096_window": ([(1, 4096), (3, 700), (1, 1)], 4, 1, 64, 600),
@@ -187,7 +195,8 @@ def test_weights_of_a_nan_query(row):
     assert torch.isfinite(acc[0, 0, seen:]).all() and torch.isfinite(acc[0, 1]).all()
 
 
-@pytest.mark.parametrize("seqs", [[(1, 900), (1, 3)], [(200, 600)]], ids=["decode", "chunk"])
+@pytest.mark.parametrize("seqs", [[(1, 900), (1, 3)], [(200, 600)], [(200, 1600)]],
+                         ids=["decode", "chunk", "pair"])
 @pytest.mark.parametrize("scale", [0.011, 4.0])
 def test_attend_scale_and_large_scores(seqs, scale):
     st = make(seqs, 8, 2, 32, seed=5, q_scale=4.0)
@@ -196,7 +205,8 @@ def test_attend_scale_and_large_scores(seqs, scale):
     check_attend(st, out, lse, reference(st, scale=float(np.float32(scale))))
 
 
-@pytest.mark.parametrize("seqs", [[(1, 700), (2, 40)], [(150, 400), (70, 70)]], ids=["decode", "chunk"])
+@pytest.mark.parametrize("seqs", [[(1, 700), (2, 40)], [(150, 400), (70, 70)], [(150, 1400), (70, 70)]],
+                         ids=["decode", "chunk", "pair"])
 def test_attend_strides_and_alias_free_rows(seqs):
     """q and out as slices of wider rows; no lse."""
     st = make(seqs, 8, 2, 16, seed=6)
@@ -236,7 +246,8 @@ def test_masked_row_and_nan_query():
     check_attend(st, out, lse, ref)
 
 
-@pytest.mark.parametrize("seqs", [[(1, 2500), (1, 20)], [(200, 1500), (1, 900)]], ids=["decode", "mixed"])
+@pytest.mark.parametrize("seqs", [[(1, 2500), (1, 20)], [(200, 1500), (1, 900)], [(200, 1200), (1, 900)]],
+                         ids=["decode", "mixed", "short"])
 def test_repeated_calls_give_identical_bits(seqs):
     st = make(seqs, 8, 2, 32, seed=9)
     a = attend(st)
@@ -683,7 +694,8 @@ def expect_device_error(what):
     fa.fa_device_status()  # cleared
 
 
-@pytest.mark.parametrize("seqs", [[(1, 900), (1, 40)], [(140, 300), (30, 40)]], ids=["decode", "chunk"])
+@pytest.mark.parametrize("seqs", [[(1, 900), (1, 40)], [(140, 300), (30, 40)], [(140, 1400), (30, 40)]],
+                         ids=["decode", "chunk", "pair"])
 @pytest.mark.parametrize("entry", [-1, 2 ** 31 - 1, "one_past"])
 def test_bad_page_is_reported_and_spares_the_others(seqs, entry):
     st = make(seqs, 4, 2, 16, seed=31)
@@ -712,8 +724,8 @@ def test_bad_page_is_reported_and_spares_the_others(seqs, entry):
     expect_device_error("page_table")
 
 
-@pytest.mark.parametrize("seqs", [[(2, 60), (3, 40), (1, 9)], [(70, 160), (60, 90), (90, 100)]],
-                         ids=["decode", "chunk"])
+@pytest.mark.parametrize("seqs", [[(2, 60), (3, 40), (1, 9)], [(70, 160), (60, 90), (90, 100)],
+                                  [(70, 1400), (60, 90), (90, 100)]], ids=["decode", "chunk", "pair"])
 @pytest.mark.parametrize("what", ["kv_long", "kv_negative", "q_descends", "q_past_total", "q_many", "q_negative"])
 def test_bad_lengths_are_reported(what, seqs):
     st = make(seqs, 4, 2, 16, seed=32)
