@@ -642,6 +642,16 @@ bool encode_pool(CUtensorMap* map, const void* pool, const fa_paged_shape& s, in
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Keys by which a call is split: those that `tokens` neighbouring tokens see in a window of up to
+// 1280, else the cache's (on the device, one token over 8 KV heads of 8000 keys, window 600: 8.7 us
+// split by the cache's, 6.6 by the window's; 24 such sequences, window 1024: 25 and 20; 64, window
+// 128: 15 and 12; with a window of 4000 one took 10 and 13). Key weights, which nothing merges, are
+// split by the cache's (64 sequences, window 600: 17 and 21).
+static int rows_span(const fa_paged_shape& s, int window, int tokens) {
+  const long long n = (long long)window + tokens;
+  return window > 0 && n <= 1280 && n < s.max_kv ? (int)n : s.max_kv;
+}
+
 // Keys a chunk, in multiples of 64: `ctas` CTAs for the longest batch the shape allows, but at
 // least 256 keys (below that the merge costs more than the chunk's own read). Real batches are
 // shorter and ragged, so the targets are many CTAs an SM: 64 sequences of up to 16384 tokens
@@ -650,16 +660,16 @@ bool encode_pool(CUtensorMap* map, const void* pool, const fa_paged_shape& s, in
 // one wave of the `resident` CTAs can read in chunks of at most 768 keys is cut to fill that wave:
 // a second, partly filled one costs as much as the first (2 sequences of 8000 keys, 8 KV heads: 19
 // us in chunks of 256, 15 in chunks of 320; 8 of 3000 25 and 20).
-static int rows_chunk(const fa_paged_shape& s, int tiles, int ctas, int resident) {
+static int rows_chunk(const fa_paged_shape& s, int keys, int tiles, int ctas, int resident) {
   const long long units = (long long)s.B * s.Hkv * tiles;
   if (resident >= 2 * units) {
-    const long long n = resident / units, c = ((s.max_kv + n - 1) / n + 63) / 64 * 64;
-    if (c >= 256 && c <= 768 && c * 48 >= s.max_kv) return (int)c;
+    const long long n = resident / units, c = ((keys + n - 1) / n + 63) / 64 * 64;
+    if (c >= 256 && c <= 768 && c * 48 >= keys) return (int)c;
   }
   const long long want = (ctas + units - 1) / units;
-  long long c = (s.max_kv + want - 1) / want;
+  long long c = (keys + want - 1) / want;
   c = (c + 63) / 64 * 64;
-  long long most = (s.max_kv + 47) / 48;  // at most 48 chunks a tile: they are merged
+  long long most = (keys + 47) / 48;  // at most 48 chunks a tile: they are merged
   most = (most + 63) / 64 * 64;
   if (c < most) c = most;
   return (int)(c < 256 ? 256 : c);
@@ -694,20 +704,22 @@ static cudaError_t attend_plan(const fa_paged_shape& s, int window, AttendPlan* 
   memset(P, 0, sizeof(*P));
   P->max_rows = a->t.tok > 0 || rows <= PR_ROWS ? PR_ROWS : 0;
   P->tiles = P->max_rows > 0 ? 1 : (int)((rows + PR_ROWS - 1) / PR_ROWS);
-  P->chunk = rows_chunk(s, P->tiles, 32 * sms, 3 * sms);
-  P->slots = chunk_slots(s, window, P->chunk, (PR_ROWS + G - 1) / G);
+  const int tokens = (PR_ROWS + G - 1) / G, keys = rows_span(s, window, tokens);
+  P->chunk = rows_chunk(s, keys, P->tiles, 32 * sms, 3 * sms);
+  P->slots = chunk_slots(s, window, P->chunk, tokens);
   P->window = window;
-  // Caches of at most 4096 tokens go in 8 chunks of at least 64 tokens that one cluster merges:
-  // the second kernel takes longer than such a chunk (one token over 2048 keys: 12 us with it, 10
-  // without). Where that makes more CTAs than are resident, single CTAs pack better than clusters
+  // Caches of at most 4096 tokens (or short windows) go in 8 chunks of at least 64 tokens that one
+  // cluster merges: the second kernel takes longer than such a chunk (one token over 2048 keys: 12
+  // us with it, 10 without). A window starts inside a chunk, so 7 chunks' length is cut. Where that makes more CTAs than are resident, single CTAs pack better than clusters
   // (8 x 8 tiles over 3000 keys: 21 us against 25). Up to 256 tokens one CTA is quicker alone.
-  if (P->max_rows > 0 && s.max_kv <= 256) {
-    P->chunk = 256;
+  if (P->max_rows > 0 && keys <= 256) {
+    P->chunk = (s.max_kv + 63) / 64 * 64;
     P->slots = 1;
-  } else if (P->max_rows > 0 && s.max_kv <= PR_CLUSTER * 512 && P->slots > 1 &&
+  } else if (P->max_rows > 0 && keys <= PR_CLUSTER * 512 && P->slots > 1 &&
       (long long)s.B * s.Hkv * PR_CLUSTER <= 3LL * sms) {
-    const int c = ((s.max_kv + PR_CLUSTER - 1) / PR_CLUSTER + 63) / 64 * 64;
-    const int n = chunk_slots(s, window, c, (PR_ROWS + G - 1) / G);
+    const int parts = keys < s.max_kv ? PR_CLUSTER - 1 : PR_CLUSTER;
+    const int c = ((keys + parts - 1) / parts + 63) / 64 * 64;
+    const int n = chunk_slots(s, window, c, tokens);
     if (n <= PR_CLUSTER) {
       P->chunk = c;
       P->slots = n;
@@ -829,7 +841,7 @@ cudaError_t launch_paged_weights(const fa_paged_shape& s, const fa_paged_cache& 
   const long long max_q = s.max_q < s.total_q ? s.max_q : s.total_q;
   const bool tiles = P.p.G <= 128 && max_q * P.p.G > PR_ROWS;
   P.max_rows = tiles ? PR_ROWS : 0;
-  P.chunk = rows_chunk(s, 1, 16 * sms, 4 * sms);
+  P.chunk = rows_chunk(s, s.max_kv, 1, 16 * sms, 4 * sms);
   P.slots = chunk_slots(s, window, P.chunk, tiles ? PR_ROWS : (int)max_q);
   CUtensorMap tk;
   if (!encode_pool(&tk, c.K, s, PR_KEYS)) {

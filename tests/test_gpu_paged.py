@@ -142,6 +142,10 @@ CASES = {
     "decode_over_4096": ([(1, 9001), (2, 4200), (1, 5)], 8, 2, 64, 0),
     "decode_4096": ([(1, 4096), (1, 1), (2, 513), (0, 9)], 8, 2, 128, 0),
     "decode_4096_window": ([(1, 4096), (3, 700), (1, 1)], 4, 1, 64, 600),
+    "decode_window_600": ([(1, 9000), (2, 8111), (1, 5), (2, 602)], 8, 2, 64, 600),
+    "decode_window_100": ([(1, 7003), (3, 500), (1, 100), (2, 101)], 4, 1, 16, 100),
+    "decode_window_1200": ([(1, 5003), (1, 1201), (1, 9)], 16, 8, 16, 1200),
+    "mixed_window": ([(1, 6000), (100, 3000), (2, 1300), (33, 700)], 8, 2, 32, 300),
     "mixed": ([(1, 1800), (140, 900), (1, 3), (260, 1500), (2, 1200)], 16, 4, 64, 0),
 }
 
