@@ -290,15 +290,22 @@ def _invalid(msg: str):
     raise FaError(FA_ERR_INVALID, msg)
 
 
+_torch = None  # held from the first call on, so that later ones do not look it up
+
+
+def _import_torch():
+    global _torch
+    import torch as _torch
+    return _torch
+
+
 def _device() -> int:
-    import torch
-    return torch.cuda.current_device()
+    return (_torch or _import_torch()).cuda.current_device()
 
 
 def _raw_stream(stream, device: int):
     if stream is None:
-        import torch
-        return torch._C._cuda_getCurrentRawStream(device)
+        return _torch._C._cuda_getCurrentRawStream(device)
     return getattr(stream, "cuda_stream", stream)
 
 
@@ -330,15 +337,14 @@ def _tensor(t, name: str, dtype, shape: tuple, device: int) -> int:
 def _rows(t, name: str, shape: tuple, device: int):
     """(pointer, elements between tokens) of a bf16 [tokens, heads, 128] tensor whose heads
     are dense."""
-    import torch
     try:
-        if t.dtype is torch.bfloat16 and t.shape == shape and t.get_device() == device:
+        if t.dtype is _torch.bfloat16 and t.shape == shape and t.get_device() == device:
             st = t.stride()
             if st[2] == 1 and (st[1] == HEAD_DIM or shape[1] == 1) or not t.numel():
                 return t.data_ptr(), st[0] if shape[0] > 1 else shape[1] * HEAD_DIM
     except AttributeError:
         pass
-    return _why(t, name, torch.bfloat16, shape, device, 2)
+    return _why(t, name, _torch.bfloat16, shape, device, 2)
 
 
 class PagedCache:
@@ -412,7 +418,7 @@ _STRIDE3 = ctypes.c_int64 * 3
 def fa_rope(rope: fa_rope_plan, x, positions, out, transpose: bool = False, stream=None) -> None:
     """Rotate x (bf16 or fp32 [B, T, H, 128], any strides of the first three axes) at int32
     positions [B, T] into ``out``; ``transpose``: the transposed map, its gradient."""
-    import torch
+    torch = _torch or _import_torch()
     dtype = FA_BF16
     if x.dtype is not torch.bfloat16:
         dtype = FA_F32
@@ -442,7 +448,6 @@ def fa_paged_append(batch: PagedBatch, k, v, q=None, q_out=None, rope: fa_rope_p
                     positions=None, stream=None) -> None:
     """Write the new tokens k, v (bf16 [total_q, Hkv, 128]) into the pages; with ``rope`` k, and
     q into q_out (bf16 [total_q, Hq, 128]), are rotated, at the cache index or ``positions``."""
-    import torch
     device = _device()
     pq = pqo = pp = None
     qs = qos = 0
@@ -451,7 +456,7 @@ def fa_paged_append(batch: PagedBatch, k, v, q=None, q_out=None, rope: fa_rope_p
     if q_out is not None:
         pqo, qos = _rows(q_out, "q_out", batch.q_shape, device)
     if positions is not None:
-        pp = _tensor(positions, "positions", torch.int32, (batch.total_q,), device)
+        pp = _tensor(positions, "positions", _torch.int32, (batch.total_q,), device)
     pk, ks = _rows(k, "k", batch.kv_shape, device)
     pv, vs = _rows(v, "v", batch.kv_shape, device)
     _check(LIB.fa_paged_append(*batch.refs, rope, pp, pq, qs, pqo, qos, pk, ks, pv, vs,
@@ -476,11 +481,10 @@ def fa_paged_attend(batch: PagedBatch, q, out, workspace=None, lse=None, window:
                     scale: float = 0.0, stream=None) -> None:
     """Causal attention of the new tokens q (bf16 [total_q, Hq, 128], rotated) over the pages,
     their own keys included, into ``out`` (same shape); lse: fp32 [total_q, Hq] or None."""
-    import torch
     device = _device()
     pq, qs = _rows(q, "q", batch.q_shape, device)
     po, os_ = _rows(out, "out", batch.q_shape, device)
-    pl = None if lse is None else _tensor(lse, "lse", torch.float32, batch.lse_shape, device)
+    pl = None if lse is None else _tensor(lse, "lse", _torch.float32, batch.lse_shape, device)
     ws, size = _workspace(workspace, device)
     _check(LIB.fa_paged_attend(*batch.refs, pq, qs, scale, window, po, os_, pl, ws, size,
                                _raw_stream(stream, device)))
@@ -490,10 +494,9 @@ def fa_paged_weights(batch: PagedBatch, q, lse, weights, window: int = 0, scale:
                      stream=None) -> None:
     """Add to ``weights`` (fp32 [B, Hkv, >= max_kv]) what each key gets from the batch's
     queries; ``lse`` as fa_paged_attend wrote it for the same arguments."""
-    import torch
     device = _device()
     pq, qs = _rows(q, "q", batch.q_shape, device)
-    pl = _tensor(lse, "lse", torch.float32, batch.lse_shape, device)
+    pl = _tensor(lse, "lse", _torch.float32, batch.lse_shape, device)
     pw, ld = _wide(weights, "weights", batch.cache, device)
     _check(LIB.fa_paged_weights(*batch.refs, pq, qs, scale, window, pl, pw, ld,
                                 _raw_stream(stream, device)))
@@ -501,9 +504,8 @@ def fa_paged_weights(batch: PagedBatch, q, lse, weights, window: int = 0, scale:
 
 def _wide(t, name: str, cache: PagedCache, device: int):
     """(pointer, last size) of a dense fp32 [B, Hkv, any] tensor."""
-    import torch
-    last = t.shape[-1] if isinstance(t, torch.Tensor) and t.dim() == 3 else None
-    return _tensor(t, name, torch.float32, (cache.B, cache.Hkv, last), device), last
+    last = t.shape[-1] if isinstance(t, _torch.Tensor) and t.dim() == 3 else None
+    return _tensor(t, name, _torch.float32, (cache.B, cache.Hkv, last), device), last
 
 
 def fa_evict_workspace_size(batch: PagedBatch, keep: int) -> int:
@@ -515,11 +517,10 @@ def fa_evict(batch: PagedBatch, weights, keep: int, dst: PagedCache, index, dst_
     """Keep at most ``keep`` tokens a sequence and KV head (the first ``sink``, the last
     ``recent``, then those of the largest ``weights``) and move them into the pages of ``dst``.
     index: int32 [B, Hkv, keep]; dst_len: int32 [B]; dst_weights: fp32 [B, Hkv, >= keep] or None."""
-    import torch
     c, device = batch.cache, _device()
     pw, wld = _wide(weights, "weights", c, device)
-    pi = _tensor(index, "index", torch.int32, (c.B, c.Hkv, keep), device)
-    pn = _tensor(dst_len, "dst_len", torch.int32, (c.B,), device)
+    pi = _tensor(index, "index", _torch.int32, (c.B, c.Hkv, keep), device)
+    pn = _tensor(dst_len, "dst_len", _torch.int32, (c.B,), device)
     pd, ld = (None, 0) if dst_weights is None else _wide(dst_weights, "dst_weights", c, device)
     ws, size = _workspace(workspace, device)
     shape = fa_paged_shape(dst.B, dst.Hkv, dst.Hkv, HEAD_DIM, dst.page_size, dst.num_pages,
