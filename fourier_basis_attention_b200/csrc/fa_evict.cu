@@ -11,8 +11,8 @@
 // two bits of the mantissa: weights fall into tens of bins, so that few lanes of a warp count
 // into the same one.
 // The move reads and writes each kept row once.
-//   Measured (B200): 131072 tokens of 8 KV heads to 16384, 140 MB, in 45 us (selection 18, move
-// 24 when each starts cold); 24 sequences of up to 8191 to 2001, 370 MB, in 78 us (15 and 59, the
+//   Measured (B200): 131072 tokens of 8 KV heads to 16384, 140 MB, in 42 us (selection 18, move
+// 24 when each starts cold); 24 sequences of up to 8191 to 2001, 370 MB, in 75 us (15 and 59, the
 // move at 95% of the measured copy bandwidth in rows of 256 bytes). The selection is a chain of
 // steps: the weights' way in 4 us, three digits of 2 to 3 (a count, a barrier, a scan), the
 // indices 3. Summing the histograms of a cluster by adding nonzero counts to the CTA that owns a
@@ -73,6 +73,7 @@ __device__ __forceinline__ void cluster_wait() {
 // One cluster of `size` CTAs a (sequence, KV head); CTA r has the tokens [r per, (r + 1) per).
 __global__ void __launch_bounds__(EV_THREADS)
     evict_select_kernel(const __grid_constant__ EvictParams P, int size, int held) {
+  wait_earlier_kernel();
   allow_next_kernel();
   extern __shared__ __align__(16) uint32_t keys[];
   // counts of a digit; their sums over the cluster, 1 / size of the bins in each CTA
@@ -331,20 +332,9 @@ cudaError_t launch_evict(const fa_paged_shape& s, const fa_paged_cache& c, const
   const void* fn = reinterpret_cast<const void*>(evict_select_kernel);
   // the limit counts the static arrays too, so it is raised for every size
   if ((e = raise_smem_limit(fn, EV_HELD * 4)) != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(s.Hkv * size), (unsigned)s.B, 1);
-  cfg.blockDim = dim3(EV_THREADS, 1, 1);
-  cfg.dynamicSmemBytes = (size_t)held * 4;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = (unsigned)size;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  void* args[] = {&P, &size, &held};
-  if ((e = cudaLaunchKernelExC(&cfg, fn, args)) != cudaSuccess) return e;
+  if ((e = launch_clusters(evict_select_kernel, dim3((unsigned)(s.Hkv * size), (unsigned)s.B), size, EV_THREADS,
+                           (size_t)held * 4, stream, P, size, held)) != cudaSuccess)
+    return e;
   const dim3 grid((unsigned)((keep + EM_ROWS - 1) / EM_ROWS), (unsigned)s.Hkv, (unsigned)s.B);
   return launch_overlapped(evict_move_kernel, grid, EM_THREADS, 0, stream, P);
 }

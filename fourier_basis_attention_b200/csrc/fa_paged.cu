@@ -175,6 +175,7 @@ __global__ void __launch_bounds__(PR_THREADS, STAGES == PR_STAGES ? 3 : 1)
                                              ~uintptr_t(1023));
   __shared__ uint64_t full[PR_WARPS][STAGES];
   __shared__ int abort_word;
+  wait_earlier_kernel();
   allow_next_kernel();
   const PagedBatch& p = P.p;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -504,6 +505,7 @@ __global__ void __launch_bounds__(PR_THREADS, STAGES == PW_STAGES ? 4 : 1)
                                              ~uintptr_t(1023));
   __shared__ uint64_t full[PR_WARPS][STAGES];
   __shared__ int abort_word;
+  wait_earlier_kernel();
   allow_next_kernel();
   const PagedBatch& p = P.p;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -771,19 +773,8 @@ cudaError_t launch_paged_attend(const fa_paged_shape& s, const fa_paged_cache& c
   const int smem = PR_WARPS * (deep ? PR_DEEP : PR_STAGES) * PR_STAGE + 1024;
   if ((e = raise_smem_limit(reinterpret_cast<const void*>(kernel), smem)) != cudaSuccess) return e;
   const dim3 grid((unsigned)(P.slots * P.tiles), (unsigned)s.Hkv, (unsigned)s.B);
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(PR_THREADS, 1, 1);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = P.cluster ? (unsigned)P.slots : 1u;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  if ((e = cudaLaunchKernelEx(&cfg, kernel, tk, tv, P)) != cudaSuccess) return e;
+  if ((e = launch_clusters(kernel, grid, P.cluster ? P.slots : 1, PR_THREADS, smem, stream, tk, tv, P)) != cudaSuccess)
+    return e;
   float* tile_o = part_o + a.rows_records * FA_HEAD_DIM;
   float2* tile_ml = part_ml + a.rows_records;
   if (a.t.tok > 0 &&
@@ -853,8 +844,7 @@ cudaError_t launch_paged_weights(const fa_paged_shape& s, const fa_paged_cache& 
   const int smem = PR_WARPS * (deep ? PW_DEEP : PW_STAGES) * PW_STAGE + 1024;
   if ((e = raise_smem_limit(reinterpret_cast<const void*>(kernel), smem)) != cudaSuccess) return e;
   const dim3 grid((unsigned)P.slots, (unsigned)s.Hkv, (unsigned)s.B);
-  kernel<<<grid, PR_THREADS, smem, stream>>>(tk, P);
-  if ((e = cudaGetLastError()) != cudaSuccess || !tiles) return e;
+  if ((e = launch_overlapped(kernel, grid, PR_THREADS, smem, stream, tk, P)) != cudaSuccess || !tiles) return e;
   return launch_weight_tiles(s, c, q, q_stride, scale, window, lse, weights, weights_ld, PR_ROWS,
                              stream, why);
 }

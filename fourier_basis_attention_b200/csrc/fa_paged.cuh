@@ -62,9 +62,11 @@ __device__ __forceinline__ void row_keys(const SeqSpan& s, int G, int window, in
   *lo = window > 0 ? max(0, first - window + 1) : 0;
 }
 
-// Overlap with the kernel launched next: it may be set up once every CTA of this one runs (or
-// has left), and waits for this one to complete where it calls wait_earlier_kernel. One that
-// needs none of its results calls it at its end, so that its completion covers both.
+// Overlap with the kernel launched next: it may be set up once every CTA of this one has called
+// allow_next_kernel (or has left), and waits for this one to complete where it calls
+// wait_earlier_kernel. The first kernel of a call waits for whatever ran before it, and only then
+// lets the next be set up: so a later kernel of the call that needs none of the first one's results
+// may wait at its end, and its completion covers both.
 __device__ __forceinline__ void allow_next_kernel() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
@@ -73,19 +75,27 @@ __device__ __forceinline__ void wait_earlier_kernel() {
 }
 // Launches a kernel that may be set up while the one before it on the stream still runs.
 template <typename... A, typename... B>
-cudaError_t launch_overlapped(void (*kernel)(A...), dim3 grid, int threads, size_t smem,
-                              cudaStream_t stream, const B&... args) {
+cudaError_t launch_clusters(void (*kernel)(A...), dim3 grid, int cluster, int threads, size_t smem,
+                            cudaStream_t stream, const B&... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = dim3((unsigned)threads, 1, 1);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)cluster;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+template <typename... A, typename... B>
+cudaError_t launch_overlapped(void (*kernel)(A...), dim3 grid, int threads, size_t smem,
+                              cudaStream_t stream, const B&... args) {
+  return launch_clusters(kernel, grid, 1, threads, smem, stream, args...);
 }
 
 __device__ __forceinline__ float exp2_approx(float x) {

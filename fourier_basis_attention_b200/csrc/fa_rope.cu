@@ -10,11 +10,12 @@
 // all heads), then walk over (token, head, item), an item being the two 16-byte vectors
 // that hold 8 (bf16) or 4 (fp32) pairs. A rot_dim whose halves are not whole vectors takes
 // items of one pair instead.
-//   Measured (B200): 2 x 16001 x 8 fp32 rows, head-major, 45 us, 262 MB, 88% of the measured copy
-// bandwidth (4 tokens a CTA; 72 us with one, 46 with eight; with two or four items of a thread on
-// their way 49, 74: fewer warps fit). The page write of 5 prompts of up to 4001 tokens, 373 MB,
-// takes 75 us with two items on their way (81 with one, 104 with four; its q, k and v rows lie
-// apart, so that a warp's accesses are 128-byte pieces).
+//   Measured (B200): 2 x 16001 x 8 fp32 rows, head-major, 45 us, 262 MB, 89% of the measured copy
+// bandwidth (47 before its set-up overlapped the kernel before it; then 4 tokens a CTA 47, one 72,
+// eight 46; with two or four items of a thread on their way 49, 74: fewer warps fit). The page write
+// of 5 prompts of up to 4001 tokens, 373 MB, takes 74 us with two items on their way (81 with one,
+// 104 with four, the same with the first loads ahead of the look-ups; its q, k and v rows lie apart,
+// so that a warp's accesses are 128-byte pieces).
 #include <math.h>
 #include <string.h>
 
@@ -172,6 +173,8 @@ __global__ void __launch_bounds__(RP_THREADS)
   using Item = RopeItem<T, VECTOR>;
   __shared__ float2 cs[RT][RP_PAIRS];
   __shared__ long long off[2][RT];
+  wait_earlier_kernel();
+  allow_next_kernel();
   const long long n0 = (long long)blockIdx.x * RT;
   const int nt = (int)min((long long)RT, n_tokens - n0);
   if (threadIdx.x < nt) {
@@ -215,6 +218,8 @@ __global__ void __launch_bounds__(RP_THREADS)
   __shared__ float2 cs[RT][RP_PAIRS];
   __shared__ long long slot_of[RT];  // row of the pools, head 0; -1: not cached, -2: no token
   __shared__ int pos_of[RT];
+  wait_earlier_kernel();
+  allow_next_kernel();
   const int t0 = blockIdx.x * RT, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (warp < RT) {
     const int t = t0 + warp;
@@ -342,10 +347,10 @@ static cudaError_t rope_typed(const RopeParams& r, int B, int T_len, int H, cons
   // 4 tokens a CTA share the set-up once they still fill every SM several times
   const bool four = n >= 16LL * sms;
   auto go = [&](auto kernel, int rt) {
-    kernel<<<(unsigned)((n + rt - 1) / rt), RP_THREADS, 0, stream>>>(
-        r, static_cast<const T*>(x), static_cast<T*>(y), positions, n, T_len, H, xs[0], xs[1], xs[2],
-        ys[0], ys[1], ys[2]);
-    return cudaGetLastError();
+    return launch_overlapped(kernel, dim3((unsigned)((n + rt - 1) / rt)), RP_THREADS, 0, stream, r,
+                             static_cast<const T*>(x), static_cast<T*>(y), positions, n, T_len, H,
+                             (long long)xs[0], (long long)xs[1], (long long)xs[2], (long long)ys[0],
+                             (long long)ys[1], (long long)ys[2]);
   };
   if (vec) return four ? go(rope_kernel<T, true, 4>, 4) : go(rope_kernel<T, true, 1>, 1);
   return four ? go(rope_kernel<T, false, 4>, 4) : go(rope_kernel<T, false, 1>, 1);
@@ -386,8 +391,7 @@ cudaError_t launch_paged_append(const fa_paged_shape& s, const fa_paged_cache& c
   if (e != cudaSuccess) return e;
   // 4 tokens a CTA share the look-ups once they still fill every SM several times
   auto go = [&](auto kernel, int rt) {
-    kernel<<<(unsigned)((s.total_q + rt - 1) / rt), RP_THREADS, 0, stream>>>(r, p, a);
-    return cudaGetLastError();
+    return launch_overlapped(kernel, dim3((unsigned)((s.total_q + rt - 1) / rt)), RP_THREADS, 0, stream, r, p, a);
   };
   const bool four = s.total_q >= 16 * sms;
   if (rope_vectors(r, RopeVec<__nv_bfloat16>::N))

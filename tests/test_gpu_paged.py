@@ -259,6 +259,50 @@ def test_repeated_calls_give_identical_bits(seqs):
     assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
 
 
+@pytest.mark.parametrize("seqs,window", [([(1, 300), (1, 77)], 0), ([(150, 400), (1, 90)], 0), ([(1, 900)], 50)],
+                         ids=["decode", "mixed", "window"])
+def test_calls_in_a_row_keep_the_order_of_the_stream(seqs, window):
+    """Each call's inputs are written by the kernel before it and overwritten by the one behind it;
+    the same calls with waits between them give the same bits."""
+    st = make(seqs, 8, 2, 16, seed=12)
+    kvs, total, B = [kv for _, kv in seqs], st["total"], len(seqs)
+    gen = torch.Generator().manual_seed(3)
+    N = 20
+    qs, ks = (torch.randn(N, total, h, D, generator=gen).to(BF).cuda() for h in (8, 2))
+    rope = fa.fa_rope_init()
+    K0, V0 = st["K"].clone(), st["V"].clone()
+
+    def run(wait):
+        st["K"].copy_(K0)
+        st["V"].copy_(V0)
+        q, k = torch.empty_like(qs[0]), torch.empty_like(ks[0])
+        lse, out = torch.empty(total, 8, device="cuda"), torch.empty_like(q)
+        w = torch.empty(B, 2, max(kvs), device="cuda")
+        index, length = torch.empty(B, 2, 40, dtype=torch.int32, device="cuda"), torch.empty(B, dtype=torch.int32, device="cuda")
+        dst = fa.PagedCache.dense(*torch.zeros(2, B, 2, 40, D, dtype=BF, device="cuda"))
+        ws = torch.empty(fa.fa_paged_attend_workspace_size(st["batch"], window) + 16, dtype=torch.uint8, device="cuda")
+        evict_ws = torch.empty(fa.fa_evict_workspace_size(st["batch"], 40) + 16, dtype=torch.uint8, device="cuda")
+        kept = []
+        torch.cuda.synchronize()
+        for i in range(N):
+            steps = [lambda: (q.copy_(qs[i]), k.copy_(ks[i]), w.zero_()),
+                     lambda: fa.fa_paged_append(st["batch"], k, k, q=q, q_out=q, rope=rope),
+                     lambda: fa.fa_paged_attend(st["batch"], q, out, ws, lse=lse, window=window),
+                     lambda: fa.fa_paged_weights(st["batch"], q, lse, w, window=window),
+                     lambda: fa.fa_evict(st["batch"], w, 40, dst, index, length, evict_ws, sink=2, recent=3),
+                     lambda: kept.append([t.clone() for t in (q, out, lse, w, index, dst.K, dst.V)]),
+                     lambda: (q.fill_(float("nan")), k.fill_(float("nan")), out.zero_(), lse.zero_(), index.zero_())]
+            for step in steps:
+                step()
+                if wait:
+                    torch.cuda.synchronize()
+        fa.fa_device_status()
+        return kept
+
+    for a, b in zip(run(True), run(False)):
+        assert all(torch.equal(x, y) for x, y in zip(a, b))
+
+
 def test_captured_graph_replays_with_new_lengths():
     """A graph captured at one set of lengths (all sequences short) gives those of another."""
     seqs = [(3, 900), (1, 33), (120, 500)]
