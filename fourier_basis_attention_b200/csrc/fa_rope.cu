@@ -8,8 +8,8 @@
 // Memory-bound: each row is read and written once. A CTA takes RT tokens: its threads first
 // put the tokens' 64 (cos, sin) pairs into shared memory (one sincospif a pair and token, shared by
 // all heads), then walk over (token, head, item), an item being the two 16-byte vectors
-// that hold 8 (bf16) or 4 (fp32) pairs. A rot_dim whose halves are not whole vectors takes
-// items of one pair instead.
+// that hold 8 (bf16) or 4 (fp32) pairs. A rot_dim whose halves are not whole vectors goes by rows
+// through shared memory instead.
 //   Measured (B200): 2 x 16001 x 8 fp32 rows, head-major, 45 us, 262 MB, 89% of the measured copy
 // bandwidth (47 before its set-up overlapped the kernel before it; then 4 tokens a CTA 47, one 72,
 // eight 46; with two or four items of a thread on their way 49, 74: fewer warps fit). The page write
@@ -89,20 +89,19 @@ struct RopeVec<__nv_bfloat16> {
   __device__ static __nv_bfloat16 put(float x) { return __float2bfloat16_rn(x); }
 };
 
-// Item `it` of a row: rotated pairs first, then the dims that pass. VECTOR: N pairs (two
-// vectors) or two vectors of passing dims; else one pair / two dims. Loads and stores are apart
-// so that a thread has several items on their way.
-template <typename T, bool VECTOR>
+// Item `it` of a row: rotated pairs first, then the dims that pass, N pairs (two vectors) or two
+// vectors of passing dims. Loads and stores are apart so that a thread has several items on their
+// way.
+template <typename T>
 struct RopeItem {
   using V = RopeVec<T>;
-  static constexpr int N = VECTOR ? V::N : 1;
+  static constexpr int N = V::N;
   static constexpr int ITEMS = RP_PAIRS / N;  // a row
   T* y;         // row written; null: no item
   const float2* cs;  // the token's pairs
   int i, da, db;     // first pair (or half the first passing dim), the two dims
   bool turn;
   typename V::Raw a, b;
-  T xa, xb;
 
   __device__ void load(const T* x, int it, int rot, int interleaved) {
     i = it * N;
@@ -113,54 +112,70 @@ struct RopeItem {
       da = i;
       db = rot / 2 + i;
     }
-    if constexpr (VECTOR) {
-      a = V::raw(x + da);
-      b = V::raw(x + db);
-    } else {
-      xa = x[da];
-      xb = x[db];
-    }
+    a = V::raw(x + da);
+    b = V::raw(x + db);
   }
   __device__ void store(int interleaved) const {
-    if constexpr (VECTOR) {
-      if (!turn) {
-        V::put_raw(y + da, a);
-        V::put_raw(y + db, b);
-        return;
-      }
-      float p[N], q[N];
-      V::split(a, p);
-      V::split(b, q);
-      if (interleaved) {
-#pragma unroll
-        for (int e = 0; e < N; e += 2) {
-          const float2 u = cs[i + e / 2], w = cs[i + (N + e) / 2];
-          const float p0 = p[e], q0 = q[e];
-          p[e] = p0 * u.x - p[e + 1] * u.y;
-          p[e + 1] = p[e + 1] * u.x + p0 * u.y;
-          q[e] = q0 * w.x - q[e + 1] * w.y;
-          q[e + 1] = q[e + 1] * w.x + q0 * w.y;
-        }
-      } else {
-#pragma unroll
-        for (int e = 0; e < N; ++e) {
-          const float2 u = cs[i + e];
-          const float p0 = p[e];
-          p[e] = p0 * u.x - q[e] * u.y;
-          q[e] = q[e] * u.x + p0 * u.y;
-        }
-      }
-      V::put_raw(y + da, V::join(p));
-      V::put_raw(y + db, V::join(q));
-    } else if (turn) {
-      const float2 u = cs[i];
-      const float p = V::get(xa), q = V::get(xb);
-      y[da] = V::put(p * u.x - q * u.y);
-      y[db] = V::put(q * u.x + p * u.y);
-    } else {
-      y[da] = xa;
-      y[db] = xb;
+    if (!turn) {
+      V::put_raw(y + da, a);
+      V::put_raw(y + db, b);
+      return;
     }
+    float p[N], q[N];
+    V::split(a, p);
+    V::split(b, q);
+    if (interleaved) {
+#pragma unroll
+      for (int e = 0; e < N; e += 2) {
+        const float2 u = cs[i + e / 2], w = cs[i + (N + e) / 2];
+        const float p0 = p[e], q0 = q[e];
+        p[e] = p0 * u.x - p[e + 1] * u.y;
+        p[e + 1] = p[e + 1] * u.x + p0 * u.y;
+        q[e] = q0 * w.x - q[e + 1] * w.y;
+        q[e + 1] = q[e + 1] * w.x + q0 * w.y;
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < N; ++e) {
+        const float2 u = cs[i + e];
+        const float p0 = p[e];
+        p[e] = p0 * u.x - q[e] * u.y;
+        q[e] = q[e] * u.x + p0 * u.y;
+      }
+    }
+    V::put_raw(y + da, V::join(p));
+    V::put_raw(y + db, V::join(q));
+  }
+};
+
+// A row whose pairs do not fall into whole vectors: 16 (bf16) or 32 (fp32) lanes take it through
+// shared memory, read and written in vectors there and back, rotated in place a pair a lane. (2 x 8001
+// x 8 rows, rot_dim 24, 62 and 100, bf16: 21, 22 and 25 us with a pair an item straight from memory,
+// 12, 15 and 23 this way; fp32, 62 and 100: 37 and 39, 29 and 31.)
+template <typename T>
+struct RopeRow {
+  using V = RopeVec<T>;
+  static constexpr int LANES = FA_HEAD_DIM / V::N;
+  static constexpr int STRIDE = FA_HEAD_DIM + 16;  // the two rows of a warp on different banks
+  static constexpr int BUF = RP_THREADS / LANES * STRIDE;
+
+  // `buf`: the CTA's; called by all LANES lanes of a row
+  __device__ static void turn(const T* x, T* y, const float2* cs, int rot, int interleaved, T* buf) {
+    const int l = threadIdx.x % LANES;
+    const unsigned lanes = LANES == 32 ? 0xFFFFFFFFu : 0xFFFFu << (threadIdx.x & 16);
+    T* row = buf + threadIdx.x / LANES * STRIDE;
+    V::put_raw(row + l * V::N, V::raw(x + l * V::N));
+    __syncwarp(lanes);
+    for (int i = l; i < rot / 2; i += LANES) {
+      const int da = interleaved ? 2 * i : i, db = interleaved ? 2 * i + 1 : rot / 2 + i;
+      const float2 u = cs[i];
+      const float p = V::get(row[da]), q = V::get(row[db]);
+      row[da] = V::put(p * u.x - q * u.y);
+      row[db] = V::put(q * u.x + p * u.y);
+    }
+    __syncwarp(lanes);
+    V::put_raw(y + l * V::N, V::raw(row + l * V::N));
+    __syncwarp(lanes);  // the lanes' next row lies there too
   }
 };
 
@@ -170,7 +185,7 @@ __global__ void __launch_bounds__(RP_THREADS)
                 const int* __restrict__ positions, long long n_tokens, int T_len, int H,
                 long long xb, long long xt, long long xh, long long yb, long long yt,
                 long long yh) {
-  using Item = RopeItem<T, VECTOR>;
+  using Item = RopeItem<T>;
   __shared__ float2 cs[RT][RP_PAIRS];
   __shared__ long long off[2][RT];
   wait_earlier_kernel();
@@ -187,15 +202,20 @@ __global__ void __launch_bounds__(RP_THREADS)
     cs[t][pair] = rope_cs(r, pair, positions[n0 + t]);
   }
   __syncthreads();
-  const int all = RT * H * Item::ITEMS;
-  for (int w = threadIdx.x; w < all; w += RP_THREADS) {
-    const int row = w / Item::ITEMS, t = row % RT, h = row / RT;
+  constexpr int ITEMS = VECTOR ? Item::ITEMS : RopeRow<T>::LANES;
+  for (int w = threadIdx.x; w < RT * H * ITEMS; w += RP_THREADS) {
+    const int row = w / ITEMS, t = row % RT, h = row / RT;
     if (t >= nt) continue;
-    Item item;
-    item.y = y + off[1][t] + h * yh;
-    item.cs = cs[t];
-    item.load(x + off[0][t] + h * xh, w % Item::ITEMS, r.rot, r.interleaved);
-    item.store(r.interleaved);
+    if constexpr (VECTOR) {
+      Item item;
+      item.y = y + off[1][t] + h * yh;
+      item.cs = cs[t];
+      item.load(x + off[0][t] + h * xh, w % ITEMS, r.rot, r.interleaved);
+      item.store(r.interleaved);
+    } else {
+      __shared__ __align__(16) T buf[RopeRow<T>::BUF];
+      RopeRow<T>::turn(x + off[0][t] + h * xh, y + off[1][t] + h * yh, cs[t], r.rot, r.interleaved, buf);
+    }
   }
 }
 
@@ -214,7 +234,8 @@ template <bool VECTOR, int RT>
 __global__ void __launch_bounds__(RP_THREADS)
     paged_append_kernel(const __grid_constant__ RopeParams r, const __grid_constant__ PagedBatch p,
                         const __grid_constant__ AppendRows a) {
-  using Item = RopeItem<__nv_bfloat16, VECTOR>;
+  using Item = RopeItem<__nv_bfloat16>;
+  using Row = RopeRow<__nv_bfloat16>;
   __shared__ float2 cs[RT][RP_PAIRS];
   __shared__ long long slot_of[RT];  // row of the pools, head 0; -1: not cached, -2: no token
   __shared__ int pos_of[RT];
@@ -253,32 +274,50 @@ __global__ void __launch_bounds__(RP_THREADS)
     cs[t][pair] = rope_cs(r, pair, pos_of[t]);
   }
   __syncthreads();
-  const int nq = a.heads - 2 * p.Hkv, all = RT * a.heads * Item::ITEMS;
-  for (int w0 = threadIdx.x; w0 < all; w0 += RP_BATCH * RP_THREADS) {
-    Item item[RP_BATCH];
-#pragma unroll
-    for (int u = 0; u < RP_BATCH; ++u) {
-      const int w = w0 + u * RP_THREADS, row = w / Item::ITEMS, t = row / a.heads, h = row - t * a.heads;
-      item[u].y = nullptr;
-      if (w >= all || slot_of[t] == -2) continue;
-      const long long token = t0 + t;
-      const __nv_bfloat16* x;
-      if (h < nq) {
-        x = a.q + token * a.q_stride + h * FA_HEAD_DIM;
-        item[u].y = a.q_out + token * a.q_out_stride + h * FA_HEAD_DIM;
-      } else {
-        if (slot_of[t] < 0) continue;
-        const int g = h - nq, gk = g < p.Hkv ? g : g - p.Hkv;
-        x = g < p.Hkv ? a.k + token * a.k_stride + gk * FA_HEAD_DIM
-                      : a.v + token * a.v_stride + gk * FA_HEAD_DIM;
-        item[u].y = (g < p.Hkv ? a.K : a.V) + (slot_of[t] + (long long)gk * p.page) * FA_HEAD_DIM;
-      }
-      item[u].cs = cs[t];
-      item[u].load(x, w % Item::ITEMS, h < nq + p.Hkv ? rot : 0, r.interleaved);
+  const int nq = a.heads - 2 * p.Hkv;
+  // where row `row` of the CTA comes from and goes to; false: nowhere
+  auto find = [&](int row, const __nv_bfloat16** x, __nv_bfloat16** y, int* t, int* turned) {
+    *t = row / a.heads;
+    const int h = row - *t * a.heads;
+    if (*t >= RT || slot_of[*t] == -2 || (h >= nq && slot_of[*t] < 0)) return false;
+    const long long token = t0 + *t;
+    *turned = h < nq + p.Hkv ? rot : 0;
+    if (h < nq) {
+      *x = a.q + token * a.q_stride + h * FA_HEAD_DIM;
+      *y = a.q_out + token * a.q_out_stride + h * FA_HEAD_DIM;
+    } else {
+      const int g = h - nq, gk = g < p.Hkv ? g : g - p.Hkv;
+      *x = g < p.Hkv ? a.k + token * a.k_stride + gk * FA_HEAD_DIM
+                     : a.v + token * a.v_stride + gk * FA_HEAD_DIM;
+      *y = (g < p.Hkv ? a.K : a.V) + (slot_of[*t] + (long long)gk * p.page) * FA_HEAD_DIM;
     }
+    return true;
+  };
+  if constexpr (VECTOR) {
+    for (int w0 = threadIdx.x; w0 < RT * a.heads * Item::ITEMS; w0 += RP_BATCH * RP_THREADS) {
+      Item item[RP_BATCH];
 #pragma unroll
-    for (int u = 0; u < RP_BATCH; ++u)
-      if (item[u].y) item[u].store(r.interleaved);
+      for (int u = 0; u < RP_BATCH; ++u) {
+        const int w = w0 + u * RP_THREADS;
+        const __nv_bfloat16* x;
+        int t, turned;
+        item[u].y = nullptr;
+        if (!find(w / Item::ITEMS, &x, &item[u].y, &t, &turned)) continue;
+        item[u].cs = cs[t];
+        item[u].load(x, w % Item::ITEMS, turned, r.interleaved);
+      }
+#pragma unroll
+      for (int u = 0; u < RP_BATCH; ++u)
+        if (item[u].y) item[u].store(r.interleaved);
+    }
+  } else {
+    __shared__ __align__(16) __nv_bfloat16 buf[Row::BUF];
+    for (int w = threadIdx.x; w < RT * a.heads * Row::LANES; w += RP_THREADS) {
+      const __nv_bfloat16* x;
+      __nv_bfloat16* y;
+      int t, turned;
+      if (find(w / Row::LANES, &x, &y, &t, &turned)) Row::turn(x, y, cs[t], turned, r.interleaved, buf);
+    }
   }
 }
 
