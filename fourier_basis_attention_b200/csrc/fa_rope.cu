@@ -10,12 +10,12 @@
 // all heads), then walk over (token, head, item), an item being the two 16-byte vectors
 // that hold 8 (bf16) or 4 (fp32) pairs. A rot_dim whose halves are not whole vectors goes by rows
 // through shared memory instead.
-//   Measured (B200): 2 x 16001 x 8 fp32 rows, head-major, 45 us, 262 MB, 89% of the measured copy
-// bandwidth (47 before its set-up overlapped the kernel before it; then 4 tokens a CTA 47, one 72,
-// eight 46; with two or four items of a thread on their way 49, 74: fewer warps fit). The page write
-// of 5 prompts of up to 4001 tokens, 373 MB, takes 74 us with two items on their way (81 with one,
-// 104 with four, the same with the first loads ahead of the look-ups; its q, k and v rows lie apart,
-// so that a warp's accesses are 128-byte pieces).
+//   Measured (B200): 2 x 16001 x 8 fp32 rows, head-major, 44 us, 262 MB, 90% of the measured copy
+// bandwidth (before its set-up overlapped the kernel before it 47, and then one token a CTA 72,
+// eight 46, two or four items of a thread on their way 49 and 74: fewer warps fit). The page write
+// of 5 prompts of up to 4001 tokens, 373 MB, takes 71 us with two items on their way (before two
+// other steps 75, and then with one 81, with four 104, the same with the first loads ahead of the
+// look-ups; its q, k and v rows lie apart, so that a warp's accesses are 128-byte pieces).
 #include <math.h>
 #include <string.h>
 
@@ -35,7 +35,11 @@ struct RopeParams {
 
 // magnitude * (cos, sin) of pair i at position pos.
 __device__ __forceinline__ float2 rope_cs(const RopeParams& r, int i, int pos) {
-  const unsigned long long phase = (unsigned long long)(long long)pos * r.turns[i];
+  // by a load and not as a constant: those of a warp's 32 pairs would be read one by one (2 x 8001 x
+  // 8 bf16 rows: 17.2 us, 14.1 this way)
+  unsigned long long turns;
+  asm("ld.b64 %0, [%1];" : "=l"(turns) : "l"(r.turns + i));
+  const unsigned long long phase = (unsigned long long)(long long)pos * turns;
   // nearest quarter turn, and the rest in [-1/4, 1/4] half turns: fp32 holds that to 2^-26
   const uint32_t turn = (uint32_t)(phase >> 32), quarter = (turn + 0x20000000u) >> 30;
   float s, c;
