@@ -6,7 +6,8 @@
 // into chunks of equal length, one CTA each; within a chunk each warp streams its own blocks
 // of 16 keys (and values) through a ring of TMA boxes and keeps its own m, l and o, so that
 // no warp waits for another until the end, when the CTA's warps merge in shared memory and
-// the chunks in a second kernel (chunk order, so repeated calls give identical bits).
+// the chunks in their cluster or in a second kernel (in a fixed order, so repeated calls give
+// identical bits).
 //
 // Few rows make this the read of K and V: 512 bytes a key and head against 16 x 512 flops on
 // warp-level bf16 MMA (m16n8k16; a 128-row tcgen05 tile would be 7/8 empty here).
