@@ -303,6 +303,54 @@ def test_calls_in_a_row_keep_the_order_of_the_stream(seqs, window):
         assert all(torch.equal(x, y) for x, y in zip(a, b))
 
 
+@pytest.mark.parametrize("seqs", [[(1, 300), (1, 77)], [(150, 400), (1, 90)]], ids=["decode", "mixed"])
+def test_capture_behind_memsets_copies_and_other_streams(seqs):
+    """Calls whose predecessors in a graph are a memset, a copy, or kernels of two streams."""
+    st = make(seqs, 8, 2, 16, seed=13)
+    total, B, longest = st["total"], len(seqs), max(kv for _, kv in seqs)
+    q, host = torch.zeros_like(st["q"]), st["q"].cpu().pin_memory()
+    out, other, lse = torch.zeros_like(q), torch.zeros_like(q), torch.zeros(total, 8, device="cuda")
+    other_lse = torch.zeros_like(lse)
+    w = torch.ones(B, 2, longest, device="cuda")
+    size = fa.fa_paged_attend_workspace_size(st["batch"]) + 16
+    ws = [torch.empty(size, dtype=torch.uint8, device="cuda") for _ in range(2)]
+    main, side = torch.cuda.Stream(), torch.cuda.Stream()
+
+    def step():
+        q.copy_(host, non_blocking=True)
+        fork = torch.cuda.Event()
+        fork.record(main)
+        side.wait_event(fork)
+        fa.fa_paged_attend(st["batch"], q, out, ws[0], lse=lse)
+        with torch.cuda.stream(side):
+            fa.fa_paged_attend(st["batch"], q, other, ws[1], lse=other_lse)
+            join = torch.cuda.Event()
+            join.record(side)
+        main.wait_event(join)
+        w.zero_()
+        fa.fa_paged_weights(st["batch"], q, other_lse, w)
+        w.mul_(2.0)
+        fa.fa_paged_weights(st["batch"], q, lse, w)
+
+    with torch.cuda.stream(main):
+        step()
+        torch.cuda.synchronize()
+        expect = [t.clone() for t in (out, other, lse, other_lse, w)]
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=main):
+            step()
+        for t in (q, out, other, lse, other_lse, w):
+            t.fill_(7.0)
+        for _ in range(5):
+            graph.replay()
+        torch.cuda.synchronize()
+    fa.fa_device_status()
+    assert torch.equal(expect[0], expect[1])
+    for t, e in zip((out, other, lse, other_lse, w), expect):
+        assert torch.equal(t, e)
+    check_attend(st, out, lse, reference(st))
+
+
 def test_captured_graph_replays_with_new_lengths():
     """A graph captured at one set of lengths (all sequences short) gives those of another."""
     seqs = [(3, 900), (1, 33), (120, 500)]
