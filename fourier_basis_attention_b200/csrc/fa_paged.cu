@@ -233,8 +233,7 @@ __global__ void __launch_bounds__(PR_THREADS, STAGES == PR_STAGES ? 3 : 1)
     const int st = i % STAGES;
     int next = 0;  // looked up while this block is on its way
     if (lane == 0 && i + STAGES < ring.n) next = ring.row_of(i + STAGES);
-    const bool ok = mbar_wait(&ring.full[st], (uint32_t)(i / STAGES) & 1u, abort_flag, WD_PAGED | 1u);
-    if (!__all_sync(0xFFFFFFFFu, ok)) {
+    if (!warp_wait(&ring.full[st], (uint32_t)(i / STAGES) & 1u, abort_flag, WD_PAGED | 1u)) {
       if (lane == 0) ring.drain(i);
       break;
     }
@@ -556,8 +555,7 @@ __global__ void __launch_bounds__(PR_THREADS, STAGES == PW_STAGES ? 4 : 1)
     const float old_next = old_weight(i + 1);
     int next = 0;
     if (lane == 0 && i + STAGES < ring.n) next = ring.row_of(i + STAGES);
-    const bool ok = mbar_wait(&ring.full[st], (uint32_t)(i / STAGES) & 1u, &abort_word, WD_PAGED | 2u);
-    if (!__all_sync(0xFFFFFFFFu, ok)) {
+    if (!warp_wait(&ring.full[st], (uint32_t)(i / STAGES) & 1u, &abort_word, WD_PAGED | 2u)) {
       if (lane == 0) ring.drain(i);
       break;
     }

@@ -62,6 +62,14 @@ __device__ __forceinline__ void row_keys(const SeqSpan& s, int G, int window, in
   *lo = window > 0 ? max(0, first - window + 1) : 0;
 }
 
+// A wait by all lanes of a warp, with one answer for all: each lane polls the barrier, the abort word
+// and the clock by itself, so that where a wait runs out lanes may differ, and a warp that branched on
+// that would meet at different votes for good.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort,
+                                          unsigned int site) {
+  return __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, abort, site));
+}
+
 // Overlap with the kernel launched next: it may be set up once every CTA of this one has called
 // allow_next_kernel (or has left), and waits for this one to complete where it calls
 // wait_earlier_kernel. The first kernel of a call waits for whatever ran before it, and only then

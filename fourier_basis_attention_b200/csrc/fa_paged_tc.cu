@@ -322,8 +322,7 @@ __device__ __forceinline__ void attend_tiles(const CUtensorMap& tq, const CUtens
           for (int v = 0; v < 2; ++v) {
             const int st = issued % STAGES;
             if (issued >= STAGES)
-              ok = mbar_wait(&empty[st], (uint32_t)(issued / STAGES - 1) & 1u, abort_flag, WD_PAGED | 3u);
-            ok = __all_sync(0xFFFFFFFFu, ok);
+              ok = warp_wait(&empty[st], (uint32_t)(issued / STAGES - 1) & 1u, abort_flag, WD_PAGED | 3u);
             if (!ok) break;
             if (lane == 0) mbar_arrive_expect_tx(&full[st], PT_BLOCK);
             __syncwarp();
@@ -353,10 +352,10 @@ __device__ __forceinline__ void attend_tiles(const CUtensorMap& tq, const CUtens
         mma_commit(&s_full[t]);
       };
       auto loaded = [&](int c) {  // use c of the ring
-        return mbar_wait(&full[c % STAGES], (uint32_t)(c / STAGES) & 1u, abort_flag, WD_PAGED | 5u);
+        return warp_wait(&full[c % STAGES], (uint32_t)(c / STAGES) & 1u, abort_flag, WD_PAGED | 5u);
       };
-      bool ok = nb > 0 && mbar_wait(&sh.q_full, 0, abort_flag, WD_PAGED | 4u) && loaded(0);
-      if (__all_sync(0xFFFFFFFFu, ok) && elect_one()) {
+      bool ok = nb > 0 && warp_wait(&sh.q_full, 0, abort_flag, WD_PAGED | 4u) && loaded(0);
+      if (ok && elect_one()) {
         if (a0 == 0 && e0 > 0) scores(0, 0);
         if (NT == 2 && a1 == 0 && e1 > 0) scores(1, 0);
         mma_commit(&empty[0]);
@@ -380,11 +379,8 @@ __device__ __forceinline__ void attend_tiles(const CUtensorMap& tq, const CUtens
             // others are still computed
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-              ok = ok && mbar_wait(&p_full[2 * t + h], (uint32_t)(i - a) & 1u, abort_flag, WD_PAGED | 6u);
-              if (!__all_sync(0xFFFFFFFFu, ok)) {
-                ok = false;
-                break;
-              }
+              ok = warp_wait(&p_full[2 * t + h], (uint32_t)(i - a) & 1u, abort_flag, WD_PAGED | 6u);
+              if (!ok) break;
               tc_fence_after();
               if (elect_one()) {
 #pragma unroll
@@ -410,10 +406,7 @@ __device__ __forceinline__ void attend_tiles(const CUtensorMap& tq, const CUtens
           }
           ok = ok && (!more || loaded(2 * i + 2));
         }
-        if (!__all_sync(0xFFFFFFFFu, ok)) {
-          ok = false;
-          break;
-        }
+        if (!ok) break;
         if (elect_one()) {
           if (NT == 2) mma_commit(&empty[sv]);
           if (NT == 1 && more && i + 1 >= a0 && i + 1 < e0) scores(0, sk);
@@ -446,8 +439,7 @@ __device__ __forceinline__ void attend_tiles(const CUtensorMap& tq, const CUtens
       float m = -INFINITY, l = 0.0f;
       bool ok = true;
       for (int i = a; i < e_; ++i) {
-        ok = mbar_wait(&s_full[t], (uint32_t)(i - a) & 1u, abort_flag, WD_PAGED | 7u);
-        ok = __all_sync(0xFFFFFFFFu, ok);
+        ok = warp_wait(&s_full[t], (uint32_t)(i - a) & 1u, abort_flag, WD_PAGED | 7u);
         if (!ok) break;
         tc_fence_after();
         uint32_t sr[4][32];
@@ -522,8 +514,7 @@ __device__ __forceinline__ void attend_tiles(const CUtensorMap& tq, const CUtens
         l += l0 + l1;
       }
       if (e_ > a && ok) {
-        ok = mbar_wait(&sh.o_full[t], 0, abort_flag, WD_PAGED | 8u);
-        ok = __all_sync(0xFFFFFFFFu, ok);
+        ok = warp_wait(&sh.o_full[t], 0, abort_flag, WD_PAGED | 8u);
         tc_fence_after();
       }
       if (ok) {
@@ -745,8 +736,7 @@ __global__ void __launch_bounds__(PV_THREADS, 1)
       for (; ok && w.next(P, lane); ++it) {
         int row[2];
         for (int t = 0; t < 2; ++t) row[t] = key_row(p, w.b, w.g, w.j0 + t * PT_TILE, P.box, w.lo, w.hi, lane);
-        if (it > 0) ok = mbar_wait(&k_empty, (uint32_t)(it - 1) & 1u, abort_flag, WD_PAGED | 14u);
-        ok = __all_sync(0xFFFFFFFFu, ok);
+        if (it > 0) ok = warp_wait(&k_empty, (uint32_t)(it - 1) & 1u, abort_flag, WD_PAGED | 14u);
         if (!ok) break;
         if (lane == 0) mbar_arrive_expect_tx(&k_full, PT_BLOCK * (1 + w.two));
         __syncwarp();
@@ -756,8 +746,7 @@ __global__ void __launch_bounds__(PV_THREADS, 1)
         for (int i = 0; i < w.nb; ++i, ++c) {
           const int st = c % PV_STAGES;
           if (c >= PV_STAGES)
-            ok = mbar_wait(&empty[st], (uint32_t)(c / PV_STAGES - 1) & 1u, abort_flag, WD_PAGED | 9u);
-          ok = __all_sync(0xFFFFFFFFu, ok);
+            ok = warp_wait(&empty[st], (uint32_t)(c / PV_STAGES - 1) & 1u, abort_flag, WD_PAGED | 9u);
           if (!ok) break;
           if (lane == 0) {
             mbar_arrive_expect_tx(&full[st], (uint32_t)(P.tok * p.G * 256));
@@ -778,17 +767,16 @@ __global__ void __launch_bounds__(PV_THREADS, 1)
       const uint32_t one_lo = desc_lo(smem_u32(ones), PV_EXTRA / 2), x_lo = desc_lo(smem_u32(extra), PV_EXTRA / 2);
       int used[2] = {0, 0};  // score buffers of each tile so far
       for (; ok && w.next(P, lane); ++it) {
-        ok = mbar_wait(&k_full, (uint32_t)it & 1u, abort_flag, WD_PAGED | 10u);
+        ok = warp_wait(&k_full, (uint32_t)it & 1u, abort_flag, WD_PAGED | 10u);
         for (int i = 0; i < w.nb; ++i, ++c) {
           const int st = c % PV_STAGES;
-          ok = ok && mbar_wait(&full[st], (uint32_t)(c / PV_STAGES) & 1u, abort_flag, WD_PAGED | 11u);
+          ok = ok && warp_wait(&full[st], (uint32_t)(c / PV_STAGES) & 1u, abort_flag, WD_PAGED | 11u);
 #pragma unroll
           for (int t = 0; t < 2; ++t) {
             if (t > w.two) break;
             const int u = used[t] & 1;
             if (used[t] >= 2)
-              ok = ok && mbar_wait(&s_empty[2 * t + u], (uint32_t)(used[t] / 2 - 1) & 1u, abort_flag, WD_PAGED | 12u);
-            ok = __all_sync(0xFFFFFFFFu, ok);
+              ok = ok && warp_wait(&s_empty[2 * t + u], (uint32_t)(used[t] / 2 - 1) & 1u, abort_flag, WD_PAGED | 12u);
             if (!ok) break;
             ++used[t];
             tc_fence_after();
@@ -847,8 +835,7 @@ __global__ void __launch_bounds__(PV_THREADS, 1)
           }
           load(i + 1, next);
           if (c >= PV_STAGES)
-            ok = mbar_wait(&empty[st], (uint32_t)(c / PV_STAGES - 1) & 1u, abort_flag, WD_PAGED | 13u);
-          ok = __all_sync(0xFFFFFFFFu, ok);
+            ok = warp_wait(&empty[st], (uint32_t)(c / PV_STAGES - 1) & 1u, abort_flag, WD_PAGED | 13u);
           if (!ok) break;
 #pragma unroll
           for (int x = 0; x < 4; ++x)
@@ -874,8 +861,7 @@ __global__ void __launch_bounds__(PV_THREADS, 1)
       uint64_t sum[2] = {0ull, 0ull};
       for (int i = 0; t <= w.two && i < w.nb; ++i, ++used) {
         const int u = used & 1;
-        ok = mbar_wait(&s_full[2 * t + u], (uint32_t)(used / 2) & 1u, abort_flag, WD_PAGED | 15u);
-        ok = __all_sync(0xFFFFFFFFu, ok);
+        ok = warp_wait(&s_full[2 * t + u], (uint32_t)(used / 2) & 1u, abort_flag, WD_PAGED | 15u);
         if (!ok) break;
         tc_fence_after();
         uint32_t sr[2][32];

@@ -1,0 +1,26 @@
+"""Rules that the paged kernels' sources keep, checked on their text: what they guard against shows
+only where a wait runs out or another compiler schedules the code."""
+import os
+import re
+
+import pytest
+
+CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))),
+                    "fourier_basis_attention_b200", "csrc")
+KERNELS = ["fa_paged.cu", "fa_paged_tc.cu"]
+
+
+def code(name):
+    """The source without comments."""
+    with open(os.path.join(CSRC, name)) as fh:
+        return re.sub(r"//[^\n]*", "", fh.read())
+
+
+@pytest.mark.parametrize("name", KERNELS)
+def test_bounded_waits_answer_for_the_whole_warp(name):
+    """Lanes give up a bounded wait one by one; a warp that branches on its own lane's answer
+    around a vote or elect.sync can wait for good."""
+    assert not re.search(r"\bmbar_wait\s*\(", code(name))
+    assert re.search(r"\bwarp_wait\s*\(", code(name))
+    helper = re.search(r"bool warp_wait\([^{]*\{(.*?)\n\}", code("fa_paged.cuh"), re.S).group(1)
+    assert re.search(r"return __all_sync\(0xFFFFFFFFu, mbar_wait\(", helper)
