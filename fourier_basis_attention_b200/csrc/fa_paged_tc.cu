@@ -479,7 +479,7 @@ __device__ __forceinline__ void attend_tiles(const CUtensorMap& tq, const CUtens
             for (int v = 0; v < 4; ++v) {
               uint32_t o[32];
               tmem_ld_32x32b_x32(to + 32 * v, o);
-              tmem_ld_wait();
+              tmem_ld_wait_for(o);
 #pragma unroll
               for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(f * __uint_as_float(o[e]));
               tmem_st_32x32b_x32(to + 32 * v, o);
@@ -527,7 +527,7 @@ __device__ __forceinline__ void attend_tiles(const CUtensorMap& tq, const CUtens
           uint32_t o[32];
           if (e_ > a) {
             tmem_ld_32x32b_x32(to + 32 * v, o);
-            tmem_ld_wait();
+            tmem_ld_wait_for(o);
           } else {
 #pragma unroll
             for (int e = 0; e < 32; ++e) o[e] = 0u;
@@ -867,7 +867,7 @@ __global__ void __launch_bounds__(PV_THREADS, 1)
         uint32_t sr[2][32];
         tmem_ld_32x32b_x32(ts + 128 * u, sr[0]);
         tmem_ld_32x32b_x32(ts + 128 * u + 32, sr[1]);
-        tmem_ld_wait();
+        tmem_ld_wait_for(sr[0], sr[1]);
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&s_empty[2 * t + u]);

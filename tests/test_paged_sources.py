@@ -24,3 +24,14 @@ def test_bounded_waits_answer_for_the_whole_warp(name):
     assert re.search(r"\bwarp_wait\s*\(", code(name))
     helper = re.search(r"bool warp_wait\([^{]*\{(.*?)\n\}", code("fa_paged.cuh"), re.S).group(1)
     assert re.search(r"return __all_sync\(0xFFFFFFFFu, mbar_wait\(", helper)
+
+
+def test_loads_from_tensor_memory_are_tied_to_their_wait():
+    """A plain wait orders memory, not the registers that the load fills: a use of them that touches
+    no memory could be scheduled before it."""
+    text = code("fa_paged_tc.cu")
+    assert not re.search(r"\btmem_ld_wait\s*\(", text)
+    body = text[text.index("void attend_tiles("):]
+    loaded = set(re.findall(r"\btmem_ld_32x32b_x32\([^;]*?,\s*(\w+(?:\[\d\])?)\);", body))
+    waited = re.findall(r"\btmem_ld_wait_for\(([^;]*)\);", body)
+    assert loaded and loaded == {name.strip() for names in waited for name in names.split(",")}
