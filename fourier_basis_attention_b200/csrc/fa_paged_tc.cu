@@ -41,7 +41,7 @@ struct Tiles {
   struct Shared {
     uint64_t full[STAGES], empty[STAGES], q_full, s_full[NT], p_full[2 * NT], o_full[NT], drained;
     uint32_t tmem;
-    int abort;
+    int abort, issued;  // copies into the ring
   };
   static constexpr int SMEM = (NT + STAGES) * PT_BLOCK + (int)sizeof(Shared);
   // Registers after setmaxnreg, a thread: the two sums must not pass what the launch gives the
@@ -227,7 +227,9 @@ __device__ __forceinline__ int tile_sequence(const PagedBatch& p, int x, int T, 
   return b;
 }
 
-// Waits (at most 0.2 s) for the last copy into each stage, so that none lands after the CTA.
+// Waits (at most 0.2 s) for the last copy into each stage, so that none lands after the CTA. Called
+// where any warp gave up a wait, once all have stopped: the producer may have issued its last copy
+// before that.
 template <int STAGES>
 __device__ __forceinline__ void drain_ring(uint64_t* full, int issued) {
   for (int s = 0; s < STAGES; ++s) {
@@ -330,11 +332,8 @@ __device__ __forceinline__ void attend_tiles(const CUtensorMap& tq, const CUtens
             ++issued;
           }
         }
-        if (!ok && lane == 0) {
-          drain_ring<STAGES>(full, issued);
-          drain_ring<1>(&sh.q_full, 1);
-        }
       }
+      if (lane == 0) sh.issued = issued;
     } else if (warp == SOFT + 1) {
       // ------------------------------------------------------------------ MMA: one warp for both
       // tiles, so that their products run one after the other and not interleaved
@@ -561,6 +560,10 @@ __device__ __forceinline__ void attend_tiles(const CUtensorMap& tq, const CUtens
   }
   tc_fence_before();
   __syncthreads();
+  if (warp == SOFT && lane == 0 && *abort_flag) {
+    drain_ring<STAGES>(full, sh.issued);
+    drain_ring<1>(&sh.q_full, 1);
+  }
   if (warp == SOFT + 1) {
     tc_fence_after();
     tmem_dealloc(tmem, 256 * NT);
@@ -686,7 +689,7 @@ __global__ void __launch_bounds__(PV_THREADS, 1)
   __shared__ uint64_t full[PV_STAGES], empty[PV_STAGES], k_full, k_empty, s_full[4], s_empty[4], drained;
   __shared__ float half_sum[2][PV_KEYS];
   __shared__ uint32_t tmem_ptr;
-  __shared__ int abort_word;
+  __shared__ int abort_word, issued[2];  // copies of query blocks, of items' keys
   const PagedBatch& p = P.p;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   allow_next_kernel();
@@ -756,9 +759,9 @@ __global__ void __launch_bounds__(PV_THREADS, 1)
           }
         }
       }
-      if (!ok && lane == 0) {
-        drain_ring<PV_STAGES>(full, c);
-        drain_ring<1>(&k_full, k_issued);
+      if (lane == 0) {
+        issued[0] = c;
+        issued[1] = k_issued;
       }
     } else if (warp == PV_SOFT + 1) {
       // ---------------------------------------------------------------- MMA
@@ -915,6 +918,10 @@ __global__ void __launch_bounds__(PV_THREADS, 1)
   }
   tc_fence_before();
   __syncthreads();
+  if (warp == PV_SOFT && lane == 0 && *abort_flag) {
+    drain_ring<PV_STAGES>(full, issued[0]);
+    drain_ring<1>(&k_full, issued[1]);
+  }
   if (warp == PV_SOFT + 1) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);

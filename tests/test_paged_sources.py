@@ -35,3 +35,17 @@ def test_loads_from_tensor_memory_are_tied_to_their_wait():
     loaded = set(re.findall(r"\btmem_ld_32x32b_x32\([^;]*?,\s*(\w+(?:\[\d\])?)\);", body))
     waited = re.findall(r"\btmem_ld_wait_for\(([^;]*)\);", body)
     assert loaded and loaded == {name.strip() for names in waited for name in names.split(",")}
+
+
+@pytest.mark.parametrize("begin,end", [("void attend_tiles(", "paged_tile_kernel("),
+                                       ("paged_weights_tile_kernel(", "FA_WATCHDOG_READER")])
+def test_copies_in_flight_are_waited_for_whichever_warp_gave_up(begin, end):
+    """The producer may be through when another warp's wait runs out: its copies are waited for
+    where all warps have met, not where the producer's own wait failed."""
+    text = code("fa_paged_tc.cu")
+    body = text[text.index(begin):]
+    body = body[:body.index(end, len(begin))]
+    joined = body.rindex("__syncthreads();")
+    drains = [m.start() for m in re.finditer(r"\bdrain_ring<", body)]
+    assert len(drains) == 2 and min(drains) > joined
+    assert "*abort_flag" in body[joined:min(drains)]
