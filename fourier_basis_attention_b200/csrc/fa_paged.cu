@@ -799,6 +799,7 @@ cudaError_t launch_paged_attend(const fa_paged_shape& s, const fa_paged_cache& c
     const long long most = (long long)(s.max_q < s.total_q ? s.max_q : s.total_q) * P.p.G;
     J.rows = most < max_rows ? (int)most : max_rows;
     const long long rows = max_rows > 0 ? (long long)s.B * s.Hkv * J.rows : (long long)s.total_q * s.Hq;
+    if (rows == 0) return cudaSuccess;  // max_q = 0: rows behind the last sequence only
     if (rows <= 4 * sms)
       return launch_overlapped(paged_join_kernel<8>, dim3((unsigned)rows), 256, 0, stream, J);
     return launch_overlapped(paged_join_kernel<1>, dim3((unsigned)((rows + 7) / 8)), 256, 0, stream, J);

@@ -1,0 +1,35 @@
+"""GPU tests of paged calls at the borders of what their shapes allow: no new tokens, no cached
+tokens, caches of many chunks, rows that share no stride."""
+import pytest
+import torch
+
+import fourier_basis_attention_b200 as fa
+from test_gpu_paged import BF, D, attend, make
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("Hq,Hkv,max_kv", [(8, 8, 100000), (8, 2, 300), (200, 1, 5000)],
+                         ids=["split", "one_chunk", "wide_group"])
+def test_batches_of_spare_rows_only(Hq, Hkv, max_kv):
+    """max_q = 0: every row lies behind the last sequence and stays as it was, also where the keys
+    of a row would be split over CTAs and joined."""
+    st = make([(0, 50), (0, 0)], Hq, Hkv, 128, seed=1, spare_rows=3, max_q=0, max_kv=max_kv)
+    out, lse = attend(st)
+    K = st["K"].clone()
+    acc = torch.full((2, Hkv, max_kv), 3.0, device="cuda")
+    fa.fa_paged_weights(st["batch"], st["q"], lse, acc)
+    k = torch.zeros(3, Hkv, D, dtype=BF, device="cuda")
+    fa.fa_paged_append(st["batch"], k, k)
+    fa.fa_device_status()
+    assert (out == 3.0).all() and (lse == 3.0).all() and (acc == 3.0).all()
+    assert torch.equal(K.nan_to_num(9.0), st["K"].nan_to_num(9.0))
+
+
+def test_new_tokens_without_max_q_are_reported():
+    """A sequence with a new token breaks the bound max_q = 0."""
+    st = make([(1, 50)], 8, 8, 128, seed=2, max_q=0, max_kv=100000)
+    attend(st)
+    with pytest.raises(fa.FaError) as e:
+        fa.fa_device_status()
+    assert e.value.code == fa.FA_ERR_DEVICE and "q_start or kv_len" in str(e.value)
