@@ -714,7 +714,7 @@ static cudaError_t attend_plan(const fa_paged_shape& s, int window, AttendPlan* 
   // us with it, 10 without). A window starts inside a chunk, so 7 chunks' length is cut. Where that makes more CTAs than are resident, single CTAs pack better than clusters
   // (8 x 8 tiles over 3000 keys: 21 us against 25). Up to 256 tokens one CTA is quicker alone.
   if (P->max_rows > 0 && keys <= 256) {
-    P->chunk = (s.max_kv + 63) / 64 * 64;
+    P->chunk = s.max_kv > 0 ? (s.max_kv + 63) / 64 * 64 : 64;
     P->slots = 1;
   } else if (P->max_rows > 0 && keys <= PR_CLUSTER * 512 && P->slots > 1 &&
       (long long)s.B * s.Hkv * PR_CLUSTER <= 3LL * sms) {

@@ -4,7 +4,7 @@ import pytest
 import torch
 
 import fourier_basis_attention_b200 as fa
-from test_gpu_paged import BF, D, attend, make
+from test_gpu_paged import BF, D, attend, check_attend, make, reference
 
 pytestmark = pytest.mark.gpu
 
@@ -33,3 +33,17 @@ def test_new_tokens_without_max_q_are_reported():
     with pytest.raises(fa.FaError) as e:
         fa.fa_device_status()
     assert e.value.code == fa.FA_ERR_DEVICE and "q_start or kv_len" in str(e.value)
+
+
+@pytest.mark.parametrize("seqs", [[(2, 0), (1, 0)], [(2, 0), (40, 0), (0, 0)]], ids=["decode", "chunk"])
+@pytest.mark.parametrize("window", [0, 7])
+def test_batches_without_cached_tokens(seqs, window):
+    """max_kv = 0: no row sees a key."""
+    st = make(seqs, 8, 2, 16, seed=3, spare_rows=2, max_kv=0)
+    out, lse = attend(st, window)
+    acc = torch.full((len(seqs), 2, 4), 3.0, device="cuda")
+    fa.fa_paged_weights(st["batch"], st["q"], lse, acc, window=window)
+    fa.fa_device_status()
+    n = st["used"]
+    assert (out[:n] == 0.0).all() and torch.isneginf(lse[:n]).all() and (acc == 3.0).all()
+    check_attend(st, out, None, reference(st, window))

@@ -49,3 +49,14 @@ def test_copies_in_flight_are_waited_for_whichever_warp_gave_up(begin, end):
     drains = [m.start() for m in re.finditer(r"\bdrain_ring<", body)]
     assert len(drains) == 2 and min(drains) > joined
     assert "*abort_flag" in body[joined:min(drains)]
+
+
+def test_the_chunk_of_a_batch_without_cached_tokens_is_not_zero():
+    """The rows kernel divides by it."""
+    plan = code("fa_paged.cu")
+    plan = plan[plan.index("static cudaError_t attend_plan("):plan.index("cudaError_t paged_attend_workspace(")]
+    one = re.search(r"keys <= 256\) \{\s*P->chunk = ([^;]*);", plan).group(1)
+    condition, some, none = re.fullmatch(r"(.*) \? (.*) : (.*)", one).groups()
+    assert condition == "s.max_kv > 0" and int(none) > 0
+    for max_kv in (1, 63, 64, 65, 256):  # C's division of whole numbers
+        assert eval(some.replace("s.max_kv", str(max_kv)).replace("/", "//")) >= max_kv
