@@ -110,11 +110,12 @@ int check_softmax(const fa_paged_shape& s, float* scale, int32_t* window) {
   return FA_OK;
 }
 
-// Strides of [n0][n1][n2][128] rows: multiples of 16 bytes, >= 0; `apart`: rows do not overlap.
+// Strides of [n0][n1][n2][128] rows: multiples of 16 bytes, >= 0; `apart`: rows do not overlap. An
+// axis of size 1 may have any.
 int check_row_strides(const int64_t* st, const int64_t* n, int elem, bool apart, const char* name) {
   if (!st) return fail(FA_ERR_INVALID, "%s_stride is NULL", name);
   for (int i = 0; i < 3; ++i)
-    if (st[i] < 0 || st[i] * elem % 16 != 0 || st[i] > (1LL << 40))
+    if (n[i] > 1 && (st[i] < 0 || st[i] > (1LL << 40) || st[i] * elem % 16 != 0))
       return fail(FA_ERR_INVALID, "%s_stride[%d]=%lld must be a multiple of 16 bytes, >= 0", name, i,
                   (long long)st[i]);
   if (!apart) return FA_OK;

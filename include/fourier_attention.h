@@ -441,7 +441,8 @@ int fa_rope_init(const fa_rope_config* config, fa_rope_plan* rope);
  * fa_rope -- rotate rows of 128 dims.
  *   x, y       device [B][T][H][128] of dtype (FA_BF16 or FA_F32), dims contiguous; the
  *              element strides of the first three axes are x_stride[3] and y_stride[3]
- *              (host), each a multiple of 16 bytes and >= 0. Rows of y must not overlap
+ *              (host), each a multiple of 16 bytes and >= 0 (that of an axis of size 1 is not
+ *              used). Rows of y must not overlap
  *              (an order of the axes exists in which each stride covers the ones inside);
  *              x may repeat rows (stride 0). y may be x with the same strides; any other
  *              overlap of the two is undefined.

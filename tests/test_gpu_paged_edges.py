@@ -4,7 +4,7 @@ import pytest
 import torch
 
 import fourier_basis_attention_b200 as fa
-from test_gpu_paged import BF, D, attend, check_attend, make, reference
+from test_gpu_paged import BF, D, attend, check_attend, check_rope, make, reference
 
 pytestmark = pytest.mark.gpu
 
@@ -47,3 +47,16 @@ def test_batches_without_cached_tokens(seqs, window):
     n = st["used"]
     assert (out[:n] == 0.0).all() and torch.isneginf(lse[:n]).all() and (acc == 3.0).all()
     check_attend(st, out, None, reference(st, window))
+
+
+@pytest.mark.parametrize("dtype", [BF, torch.float32], ids=["bf16", "f32"])
+def test_rope_of_a_transposed_column(dtype):
+    """The strides of axes of size 1 may be anything: a [1, 1, 1, 128] view has 1 there."""
+    x = torch.randn(D, 1, device="cuda").to(dtype).t()[None, None]
+    y = torch.zeros(D, 1, dtype=dtype, device="cuda").t()[None, None]
+    assert x.stride(2) == 1 and y.stride(2) == 1
+    pos = torch.tensor([[77]], dtype=torch.int32, device="cuda")
+    fa.fa_rope(fa.fa_rope_init(), x, pos, y)
+    fa.fa_device_status()
+    check_rope(y.cpu().double().numpy(), x.cpu().double().numpy(), pos.cpu().numpy(), D, {}, False, False,
+               dtype == BF)
