@@ -309,6 +309,14 @@ def _raw_stream(stream, device: int):
     return getattr(stream, "cuda_stream", stream)
 
 
+def _here(pages, name: str = "the batch") -> int:
+    """The current device, where the pointers that a PagedBatch or PagedCache holds must lie."""
+    device = _device()
+    if pages.device != device:
+        _invalid(f"{name} is on cuda:{pages.device}, not on the current CUDA device")
+    return device
+
+
 def _why(t, name: str, dtype, shape, device: int, dense: int):
     """Raise for a tensor that _tensor refused."""
     import torch
@@ -358,7 +366,7 @@ class PagedCache:
                                      (page_table, "page_table", torch.int32, 2)):
             if not isinstance(t, torch.Tensor) or t.dim() != dims:
                 _why(t, name, dtype, (None,) * dims, -1, dims)
-        device = _device() if K.is_cuda else -2
+        device = self.device = _device() if K.is_cuda else -2
         shape = (*K.shape[:3], HEAD_DIM)
         self.pointers = (_tensor(K, "K", torch.bfloat16, shape, device),
                          _tensor(V, "V", torch.bfloat16, shape, device),
@@ -382,7 +390,7 @@ class PagedBatch:
     def __init__(self, cache: PagedCache, Hq: int, q_start, kv_len, total_q: int, max_q: int,
                  max_kv: int | None = None):
         import torch
-        device = _device()
+        device = self.device = _here(cache, "the cache")
         starts = _tensor(q_start, "q_start", torch.int32, (cache.B + 1,), device)
         lens = _tensor(kv_len, "kv_len", torch.int32, (cache.B,), device)
         self.cache, self.q_start, self.kv_len = cache, q_start, kv_len
@@ -448,7 +456,7 @@ def fa_paged_append(batch: PagedBatch, k, v, q=None, q_out=None, rope: fa_rope_p
                     positions=None, stream=None) -> None:
     """Write the new tokens k, v (bf16 [total_q, Hkv, 128]) into the pages; with ``rope`` k, and
     q into q_out (bf16 [total_q, Hq, 128]), are rotated, at the cache index or ``positions``."""
-    device = _device()
+    device = _here(batch)
     pq = pqo = pp = None
     qs = qos = 0
     if q is not None:
@@ -481,7 +489,7 @@ def fa_paged_attend(batch: PagedBatch, q, out, workspace=None, lse=None, window:
                     scale: float = 0.0, stream=None) -> None:
     """Causal attention of the new tokens q (bf16 [total_q, Hq, 128], rotated) over the pages,
     their own keys included, into ``out`` (same shape); lse: fp32 [total_q, Hq] or None."""
-    device = _device()
+    device = _here(batch)
     pq, qs = _rows(q, "q", batch.q_shape, device)
     po, os_ = _rows(out, "out", batch.q_shape, device)
     pl = None if lse is None else _tensor(lse, "lse", _torch.float32, batch.lse_shape, device)
@@ -494,7 +502,7 @@ def fa_paged_weights(batch: PagedBatch, q, lse, weights, window: int = 0, scale:
                      stream=None) -> None:
     """Add to ``weights`` (fp32 [B, Hkv, >= max_kv]) what each key gets from the batch's
     queries; ``lse`` as fa_paged_attend wrote it for the same arguments."""
-    device = _device()
+    device = _here(batch)
     pq, qs = _rows(q, "q", batch.q_shape, device)
     pl = _tensor(lse, "lse", _torch.float32, batch.lse_shape, device)
     pw, ld = _wide(weights, "weights", batch.cache, device)
@@ -517,7 +525,8 @@ def fa_evict(batch: PagedBatch, weights, keep: int, dst: PagedCache, index, dst_
     """Keep at most ``keep`` tokens a sequence and KV head (the first ``sink``, the last
     ``recent``, then those of the largest ``weights``) and move them into the pages of ``dst``.
     index: int32 [B, Hkv, keep]; dst_len: int32 [B]; dst_weights: fp32 [B, Hkv, >= keep] or None."""
-    c, device = batch.cache, _device()
+    c, device = batch.cache, _here(batch)
+    _here(dst, "dst")
     pw, wld = _wide(weights, "weights", c, device)
     pi = _tensor(index, "index", _torch.int32, (c.B, c.Hkv, keep), device)
     pn = _tensor(dst_len, "dst_len", _torch.int32, (c.B,), device)
