@@ -309,6 +309,20 @@ def _raw_stream(stream, device: int):
     return getattr(stream, "cuda_stream", stream)
 
 
+def _int32(**values) -> None:
+    """Refuse whole numbers that ctypes would cut to other ones."""
+    for name, n in values.items():
+        if not -2 ** 31 <= n < 2 ** 31:
+            _invalid(f"{name}={n} does not fit 32 bits")
+
+
+def _softmax(window: int, scale: float) -> None:
+    if not -2 ** 31 <= window < 2 ** 31:
+        _int32(window=window)
+    if 0.0 < abs(scale) < 1e-37:  # fp32 would make 0 of it, which picks 1 / sqrt(128)
+        raise FaError(FA_ERR_UNSUPPORTED, f"scale={scale} is outside [1e-20, 1e20]")
+
+
 def _here(pages, name: str = "the batch") -> int:
     """The current device, where the pointers that a PagedBatch or PagedCache holds must lie."""
     device = _device()
@@ -398,6 +412,7 @@ class PagedBatch:
         if max_kv is None:
             max_kv = cache.max_pages * cache.page_size
         self.max_kv = max_kv
+        _int32(Hq=Hq, total_q=total_q, max_q=max_q, max_kv=max_kv)
         self.shape = fa_paged_shape(cache.B, Hq, cache.Hkv, HEAD_DIM, cache.page_size,
                                     cache.num_pages, cache.max_pages, total_q, max_q, max_kv)
         self.c = fa_paged_cache(*cache.pointers, starts, lens)
@@ -413,6 +428,7 @@ def fa_rope_init(rot_dim: int = HEAD_DIM, base: float = 10000.0, interleaved: bo
     """Host-side plan of a rotation (see the C header for the scalings)."""
     if scaling not in ROPE_SCALINGS:
         _invalid(f"unknown scaling {scaling!r}")
+    _int32(rot_dim=rot_dim, original_len=original_len)
     config = fa_rope_config(rot_dim, int(bool(interleaved)), ROPE_SCALINGS[scaling], original_len,
                             base, factor, low, high, magnitude)
     plan = fa_rope_plan()
@@ -472,6 +488,7 @@ def fa_paged_append(batch: PagedBatch, k, v, q=None, q_out=None, rope: fa_rope_p
 
 
 def fa_paged_attend_workspace_size(batch: PagedBatch, window: int = 0) -> int:
+    _softmax(window, 0.0)
     return LIB.fa_paged_attend_workspace_size(batch.refs[0], window)
 
 
@@ -490,6 +507,7 @@ def fa_paged_attend(batch: PagedBatch, q, out, workspace=None, lse=None, window:
     """Causal attention of the new tokens q (bf16 [total_q, Hq, 128], rotated) over the pages,
     their own keys included, into ``out`` (same shape); lse: fp32 [total_q, Hq] or None."""
     device = _here(batch)
+    _softmax(window, scale)
     pq, qs = _rows(q, "q", batch.q_shape, device)
     po, os_ = _rows(out, "out", batch.q_shape, device)
     pl = None if lse is None else _tensor(lse, "lse", _torch.float32, batch.lse_shape, device)
@@ -503,6 +521,7 @@ def fa_paged_weights(batch: PagedBatch, q, lse, weights, window: int = 0, scale:
     """Add to ``weights`` (fp32 [B, Hkv, >= max_kv]) what each key gets from the batch's
     queries; ``lse`` as fa_paged_attend wrote it for the same arguments."""
     device = _here(batch)
+    _softmax(window, scale)
     pq, qs = _rows(q, "q", batch.q_shape, device)
     pl = _tensor(lse, "lse", _torch.float32, batch.lse_shape, device)
     pw, ld = _wide(weights, "weights", batch.cache, device)
@@ -517,6 +536,7 @@ def _wide(t, name: str, cache: PagedCache, device: int):
 
 
 def fa_evict_workspace_size(batch: PagedBatch, keep: int) -> int:
+    _int32(keep=keep)
     return LIB.fa_evict_workspace_size(batch.refs[0], keep)
 
 
@@ -527,13 +547,16 @@ def fa_evict(batch: PagedBatch, weights, keep: int, dst: PagedCache, index, dst_
     index: int32 [B, Hkv, keep]; dst_len: int32 [B]; dst_weights: fp32 [B, Hkv, >= keep] or None."""
     c, device = batch.cache, _here(batch)
     _here(dst, "dst")
+    _int32(keep=keep, sink=sink, recent=recent)
     pw, wld = _wide(weights, "weights", c, device)
     pi = _tensor(index, "index", _torch.int32, (c.B, c.Hkv, keep), device)
     pn = _tensor(dst_len, "dst_len", _torch.int32, (c.B,), device)
     pd, ld = (None, 0) if dst_weights is None else _wide(dst_weights, "dst_weights", c, device)
     ws, size = _workspace(workspace, device)
+    # the table may have room for more tokens than a shape can state: it holds `keep` or what it can
+    room = min(dst.max_pages * dst.page_size, keep)
     shape = fa_paged_shape(dst.B, dst.Hkv, dst.Hkv, HEAD_DIM, dst.page_size, dst.num_pages,
-                           dst.max_pages, 0, 0, dst.max_pages * dst.page_size)
+                           dst.max_pages, 0, 0, room)
     cache = fa_paged_cache(*dst.pointers, None, None)
     _check(LIB.fa_evict(*batch.refs, pw, wld, keep, sink, recent, ctypes.byref(shape),
                         ctypes.byref(cache), pd, ld, pi, pn, ws, size, _raw_stream(stream, device)))
