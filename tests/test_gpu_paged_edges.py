@@ -60,3 +60,18 @@ def test_rope_of_a_transposed_column(dtype):
     fa.fa_device_status()
     check_rope(y.cpu().double().numpy(), x.cpu().double().numpy(), pos.cpu().numpy(), D, {}, False, False,
                dtype == BF)
+
+
+@pytest.mark.parametrize("row", [0, 1, 6, 7, 14, 63, 70, 127, 134, 255])
+def test_weight_of_the_one_row_that_counts_is_exact(row):
+    """Scores 0 and a log-sum-exp of 0: the row gives exp(0) = 1 to every key that it sees, whichever
+    unit takes the exponential; the others (log-sum-exp 10000) give less than 2^-24."""
+    st = make([(256, 1000)], 1, 1, 32, seed=row)
+    st["q"].zero_()
+    lse = torch.full((256, 1), 10000.0, device="cuda")
+    lse[row] = 0.0
+    acc = torch.zeros(1, 1, 1000, device="cuda")
+    fa.fa_paged_weights(st["batch"], st["q"], lse, acc)
+    fa.fa_device_status()
+    seen = 1000 - 256 + row + 1
+    assert (acc[0, 0, :seen] == 1.0).all() and (acc[0, 0, seen:] < 2.0 ** -24).all()
