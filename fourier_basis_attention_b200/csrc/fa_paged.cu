@@ -661,18 +661,19 @@ static int rows_span(const fa_paged_shape& s, int window, int tokens) {
 // one wave of the `resident` CTAs can read in chunks of at most 768 keys is cut to fill that wave:
 // a second, partly filled one costs as much as the first (2 sequences of 8000 keys, 8 KV heads: 19
 // us in chunks of 256, 15 in chunks of 320; 8 of 3000 25 and 20).
-static int rows_chunk(const fa_paged_shape& s, int keys, int tiles, int ctas, int resident) {
+//   `merged`: partial results that a second kernel reads, so at most 48 chunks a tile (one token over
+// 30000 keys, 8 KV heads: 35 us in 118 chunks, 27 in 48). Key weights merge nothing (one token over
+// 131072 keys, 1 KV head: 49 us in 48 chunks, 18 in 512; 8 KV heads and a window of 4096: 42 and 16).
+static int rows_chunk(const fa_paged_shape& s, int keys, int tiles, int ctas, int resident, bool merged) {
   const long long units = (long long)s.B * s.Hkv * tiles;
+  const int most = merged ? 48 : keys;  // chunks a tile
   if (resident >= 2 * units) {
     const long long n = resident / units, c = ((keys + n - 1) / n + 63) / 64 * 64;
-    if (c >= 256 && c <= 768 && c * 48 >= keys) return (int)c;
+    if (c >= 256 && c <= 768 && c * most >= keys) return (int)c;
   }
   const long long want = (ctas + units - 1) / units;
-  long long c = (keys + want - 1) / want;
-  c = (c + 63) / 64 * 64;
-  long long most = (keys + 47) / 48;  // at most 48 chunks a tile: they are merged
-  most = (most + 63) / 64 * 64;
-  if (c < most) c = most;
+  const long long n = want < most ? want : most;
+  const long long c = n > 0 ? ((keys + n - 1) / n + 63) / 64 * 64 : 0;
   return (int)(c < 256 ? 256 : c);
 }
 
@@ -706,7 +707,7 @@ static cudaError_t attend_plan(const fa_paged_shape& s, int window, AttendPlan* 
   P->max_rows = a->t.tok > 0 || rows <= PR_ROWS ? PR_ROWS : 0;
   P->tiles = P->max_rows > 0 ? 1 : (int)((rows + PR_ROWS - 1) / PR_ROWS);
   const int tokens = (PR_ROWS + G - 1) / G, keys = rows_span(s, window, tokens);
-  P->chunk = rows_chunk(s, keys, P->tiles, 32 * sms, 3 * sms);
+  P->chunk = rows_chunk(s, keys, P->tiles, 32 * sms, 3 * sms, true);
   P->slots = chunk_slots(s, window, P->chunk, tokens);
   P->window = window;
   // Caches of at most 4096 tokens (or short windows) go in 8 chunks of at least 64 tokens that one
@@ -832,7 +833,7 @@ cudaError_t launch_paged_weights(const fa_paged_shape& s, const fa_paged_cache& 
   const long long max_q = s.max_q < s.total_q ? s.max_q : s.total_q;
   const bool tiles = P.p.G <= 128 && max_q * P.p.G > PR_ROWS;
   P.max_rows = tiles ? PR_ROWS : 0;
-  P.chunk = rows_chunk(s, s.max_kv, 1, 16 * sms, 4 * sms);
+  P.chunk = rows_chunk(s, s.max_kv, 1, 16 * sms, 4 * sms, false);
   P.slots = chunk_slots(s, window, P.chunk, tiles ? PR_ROWS : (int)max_q);
   CUtensorMap tk;
   if (!encode_pool(&tk, c.K, s, PR_KEYS)) {

@@ -4,6 +4,7 @@ import pytest
 import torch
 
 import fourier_basis_attention_b200 as fa
+import test_gpu_paged as tgp
 from test_gpu_paged import BF, D, attend, check_attend, check_rope, make, reference
 
 pytestmark = pytest.mark.gpu
@@ -75,3 +76,28 @@ def test_weight_of_the_one_row_that_counts_is_exact(row):
     fa.fa_device_status()
     seen = 1000 - 256 + row + 1
     assert (acc[0, 0, :seen] == 1.0).all() and (acc[0, 0, seen:] < 2.0 ** -24).all()
+
+
+# caches of more than 12288 keys: above that the keys of 16-row tiles are cut into 48 chunks where
+# partial results are merged, and into as many as fill the launch where none are
+LONG = {
+    "one_head": ([(1, 131077)], 4, 1, 64, 0),
+    "one_head_window": ([(1, 40001), (2, 12289)], 4, 1, 16, 4097),
+    "two_heads": ([(1, 30011), (3, 20000), (1, 7)], 8, 2, 64, 0),
+    "two_heads_window_700": ([(2, 50021), (1, 13001)], 8, 2, 128, 700),
+    "tiles": ([(40, 14001), (1, 16400)], 8, 2, 64, 0),
+    "tiles_window": ([(40, 20003), (5, 14001), (1, 300)], 8, 2, 64, 4097),
+    "wide_group": ([(2, 13007)], 160, 1, 64, 0),
+}
+
+
+@pytest.mark.parametrize("name", LONG)
+def test_attend_over_long_caches(name, monkeypatch):
+    monkeypatch.setitem(tgp.CASES, name, LONG[name])
+    tgp.test_attend(name)
+
+
+@pytest.mark.parametrize("name", LONG)
+def test_weights_over_long_caches(name, monkeypatch):
+    monkeypatch.setitem(tgp.CASES, name, LONG[name])
+    tgp.test_weights(name)
