@@ -1,5 +1,6 @@
 """GPU tests of paged calls at the borders of what their shapes allow: no new tokens, no cached
 tokens, caches of many chunks, rows that share no stride."""
+import numpy as np
 import pytest
 import torch
 
@@ -101,3 +102,15 @@ def test_attend_over_long_caches(name, monkeypatch):
 def test_weights_over_long_caches(name, monkeypatch):
     monkeypatch.setitem(tgp.CASES, name, LONG[name])
     tgp.test_weights(name)
+
+
+@pytest.mark.parametrize("seqs,window", [([(4, 2), (1, 0), (20, 5), (2, 9)], 0), ([(40, 0), (30, 10), (1, 3)], 7),
+                                         ([(1, 500), (60, 200)], 0)], ids=["few", "window", "all_see"])
+def test_rows_without_a_key_and_no_others_have_an_infinite_lse(seqs, window):
+    st = make(seqs, 8, 2, 16, seed=4, spare_rows=2)
+    out, lse = attend(st, window)
+    fa.fa_device_status()
+    n, want = st["used"], np.isneginf(reference(st, window)[2])
+    got = lse.cpu().numpy()
+    assert np.array_equal(np.isneginf(got[:n]), want[:n]) and np.isfinite(got[:n][~want[:n]]).all()
+    assert not out.cpu().float().numpy()[:n][want[:n]].any()
