@@ -9,6 +9,12 @@
 // the chunks in their cluster or in a second kernel (in a fixed order, so repeated calls give
 // identical bits).
 //
+// P is rounded to bf16 for the product with V: the tensor cores take both operands in one type, and
+// a second product with what the rounding left would double their work in the 128-row tiles. The sum
+// l is of the unrounded weights, which the log-sum-exp needs. After the output's own rounding to bf16
+// (1.65e-3 of it, root mean square) the error against 64 bits grows by 0.1% (one token over 2048
+// keys) to 2% (701 tokens, window 1024).
+//
 // Few rows make this the read of K and V: 512 bytes a key and head against 16 x 512 flops on
 // warp-level bf16 MMA (m16n8k16; a 128-row tcgen05 tile would be 7/8 empty here).
 #include <math.h>
@@ -646,8 +652,9 @@ bool encode_pool(CUtensorMap* map, const void* pool, const fa_paged_shape& s, in
 // Keys by which a call is split: those that `tokens` neighbouring tokens see in a window of up to
 // 1280, else the cache's (on the device, one token over 8 KV heads of 8000 keys, window 600: 8.7 us
 // split by the cache's, 6.6 by the window's; 24 such sequences, window 1024: 25 and 20; 64, window
-// 128: 15 and 12; with a window of 4000 one took 10 and 13). Key weights, which nothing merges, are
-// split by the cache's (64 sequences, window 600: 17 and 21).
+// 128: 15 and 12; with a window of 4000 one took 10 and 13). All of these were caches of 8000 keys: over
+// 131072, where 48 chunks of the cache leave 24 CTAs to a window of 4096, one token takes 47 us. Key
+// weights, which nothing merges, are split by the cache's (64 sequences, window 600: 17 and 21).
 static int rows_span(const fa_paged_shape& s, int window, int tokens) {
   const long long n = (long long)window + tokens;
   return window > 0 && n <= 1280 && n < s.max_kv ? (int)n : s.max_kv;
@@ -658,7 +665,8 @@ static int rows_span(const fa_paged_shape& s, int window, int tokens) {
 // shorter and ragged, so the targets are many CTAs an SM: 64 sequences of up to 16384 tokens
 // decode in 452, 366, 345, 356 us for 2, 8, 32, 64 a SM (3 are resident); key weights of 32
 // sequences of up to 8192 take 68, 63, 63, 68 us for 8, 16, 32, 64 (4 are resident). A batch that
-// one wave of the `resident` CTAs can read in chunks of at most 768 keys is cut to fill that wave:
+// one wave of the `resident` CTAs can read in chunks of at most 768 keys (and few enough of them where
+// they are merged) is cut to fill that wave:
 // a second, partly filled one costs as much as the first (2 sequences of 8000 keys, 8 KV heads: 19
 // us in chunks of 256, 15 in chunks of 320; 8 of 3000 25 and 20).
 //   `merged`: partial results that a second kernel reads, so at most 48 chunks a tile (one token over

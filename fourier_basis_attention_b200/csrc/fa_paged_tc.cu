@@ -4,7 +4,8 @@
 // An SM works on two tiles of 128 rows and streams the keys and values of their KV head in
 // blocks of 128 through a ring of TMA boxes. Per block and tile: S = Q K^T into tensor memory, one
 // thread a row turns S into weights P = exp2(c s - m) (running reference m, running sum l),
-// writes P back over S in bf16, and O += P V reads P from tensor memory. While one tile's
+// writes P back over S in bf16 (the tensor core takes both operands in one type; what that costs is
+// said at the 16-row tiles), and O += P V reads P from tensor memory. While one tile's
 // threads work on their weights the tensor core works on the other tile. The two are one CTA's,
 // which share each block, or two CTAs', of which one starts or ends while the other computes.
 //   The reference m follows the running maximum only when it falls behind by 2^8: the weights
@@ -969,10 +970,10 @@ int key_box(const fa_paged_shape& s) {
 
 // Tiles are used where some sequence may have more rows than one 16-row tile and the heads of
 // a token fit a 128-row tile. CTAs of one tile, two an SM, where a tile sees at most 10 blocks, of
-// which its start and end would take 4, or no sequence fills more than one (6 chunks with a window
-// of 1024: 97 us with two tiles a CTA, 90 with one; 1000 tokens over themselves 26 and 24; 64 x 30
-// over 4000 keys 150 and 131); else CTAs of two, which read each block once (4 x 300 over 2000 keys
-// 41 and 45; 4096 over 16384 818 and 938).
+// which its start and end would take 4, or no sequence fills more than one; else CTAs of two, which
+// read each block once. Back to back, one tile a CTA and two: 6 chunks with a window of 1024 96 and 97
+// us, 1000 tokens over themselves 24 and 25, 32 prompts of 128 40 and 48, 64 x 30 over 4000 keys 169 and
+// 251; 4 x 300 over 2000 keys 71 and 71, 1000 over 2000 41 and 40, 4096 over 16384 1053 and 924.
 //   Keys (of the window, where there is one) are split when the tiles of the batch leave SMs idle:
 // into chunks of equal length, multiples of a block and at least 2, that fill one wave. More waves
 // do not pay: the parts are written and read again (600 tokens over 4000 keys, 80 pairs of tiles:

@@ -350,7 +350,9 @@ int fa_select_dims(const float* scores, int32_t Hkv, int32_t n_compressed, uint8
  * rotated into queries and keys, keys and values are written into pages, the new tokens
  * attend over the pages, and the attention weight that each key has gathered decides which
  * tokens stay. A dense [B][Hkv][L][128] tensor, what fa_compress reads, is a pool of B
- * pages of L tokens, so fa_evict moves a paged cache into it.)
+ * pages of L tokens, so fa_evict with keep = L moves a paged cache into it. fa_compress has one L
+ * for the batch and reads all L rows: the sequences of that batch must have at least L cached
+ * tokens, or fa_evict leaves slots of them unwritten.)
  *
  * Pools. K and V are bf16 [num_pages][Hkv][page_size][128]. Token j of sequence b is slot
  *   j % page_size of page page_table[b][j / page_size].
