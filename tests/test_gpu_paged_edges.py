@@ -1,5 +1,7 @@
 """GPU tests of paged calls at the borders of what their shapes allow: no new tokens, no cached
 tokens, caches of many chunks, rows that share no stride."""
+import threading
+
 import numpy as np
 import pytest
 import torch
@@ -114,3 +116,54 @@ def test_rows_without_a_key_and_no_others_have_an_infinite_lse(seqs, window):
     got = lse.cpu().numpy()
     assert np.array_equal(np.isneginf(got[:n]), want[:n]) and np.isfinite(got[:n][~want[:n]]).all()
     assert not out.cpu().float().numpy()[:n][want[:n]].any()
+
+
+# one page a sequence, of any size: a block of keys that starts in it may end in the next head's or
+# sequence's page, or behind the pool
+DENSE = {
+    "tiny": ([(3, 5), (1, 1), (0, 4), (2, 2)], 4, 2, 5, 0),
+    "tiles_100": ([(40, 100), (33, 77), (1, 5), (20, 3)], 8, 2, 100, 0),
+    "tiles_333_window": ([(200, 333), (1, 300), (17, 129)], 4, 4, 333, 50),
+    "pair_1501": ([(300, 1501), (1, 1499), (150, 150)], 8, 2, 1501, 0),
+    "decode_5003": ([(1, 5003), (2, 4999), (1, 1)], 8, 2, 5003, 0),
+    "decode_777_window": ([(1, 777), (4, 700)], 4, 1, 777, 100),
+}
+MANY = {
+    "sequences": ([(1 + (i % 7 == 3), 1 + (13 * i) % 40) for i in range(2500)], 4, 2, 16, 0),
+    "sequences_and_chunks": ([(30 if i % 97 == 5 else i % 3, 1 + (29 * i) % 70) for i in range(1500)], 4, 2, 16, 9),
+}
+
+
+@pytest.mark.parametrize("name", [*DENSE, *MANY])
+def test_attend_over_dense_caches_and_many_sequences(name, monkeypatch):
+    monkeypatch.setitem(tgp.CASES, name, {**DENSE, **MANY}[name])
+    tgp.test_attend(name)
+
+
+@pytest.mark.parametrize("name", [*DENSE, *MANY])
+def test_weights_over_dense_caches_and_many_sequences(name, monkeypatch):
+    monkeypatch.setitem(tgp.CASES, name, {**DENSE, **MANY}[name])
+    tgp.test_weights(name)
+
+
+def test_host_threads_at_once():
+    """Calls from several host threads, a stream and a workspace each."""
+    sts = [make([(1, 2000 + 50 * i), (60, 300)], 8, 2, 32, seed=20 + i) for i in range(4)]
+    streams = [torch.cuda.Stream() for _ in sts]
+    res = [None] * len(sts)
+    torch.cuda.synchronize()
+
+    def work(i):
+        with torch.cuda.stream(streams[i]):
+            for _ in range(10):
+                res[i] = attend(sts[i])
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(len(sts))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    fa.fa_device_status()
+    for st, (out, lse) in zip(sts, res):
+        check_attend(st, out, lse, reference(st))
